@@ -348,6 +348,189 @@ SSD_API ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const f
                                   float *ddt, float *dA, void *dB, void *dC, float *dD, float *dinit_state,
                                   void *stream);
 
+/*
+ * The gated linear recurrence -- the per-channel sibling of the SSD recurrence
+ * (one number of state a channel, the decay chosen by a gate of the input).
+ * Per row b and channel c, with s(v) = 1 / (1 + e^-v):
+ *
+ *     l_t = A_c s(r_t),  a_t = exp(l_t),  m_t = sqrt(1 - a_t^2)
+ *     h_t = a_t h_{t-1} + m_t s(i_t) x_t,   y_t = h_t
+ *
+ * A is the per-channel decay rate (A_c <= 0, as A of ssd_forward is; a channel
+ * with A_c > 0 comes out as NaN).  Sizes: any batch, seqlen, channels >= 1
+ * (no alignment of any of them) with seqlen <= 2^30, channels <= 2^24 and
+ * fewer than 2^31 tiles of 64 channels and SSD_GLR_CHUNK tokens (else
+ * SSD_ERR_UNSUPPORTED); dtype is the storage type of x, r, i, y and their
+ * gradients, A, states and dA are fp32.  States and sums are held in fp32;
+ * every pass gives the same bits for the same inputs.
+ */
+typedef struct {
+    int64_t batch;    /* B */
+    int64_t seqlen;   /* T */
+    int64_t channels; /* C */
+    int32_t dtype;    /* ssd_dtype_t */
+    int32_t reserved; /* must be 0 */
+} ssd_glr_dims_t;
+
+/* Tokens between two states that ssd_glr_forward keeps for ssd_glr_backward. */
+#define SSD_GLR_CHUNK 64
+
+/*
+ * An activation checkpoint in 8 bits: rows x cols values in blocks of
+ * SSD_PACK8_BLOCK consecutive values of a row (the last block of a row may be
+ * shorter), one signed byte a value and one exponent byte a block.  A value
+ * reads back as codes * 2^(exps - 127).  The exponent is the smallest (from 1)
+ * with which the block's largest magnitude is below 127.5 steps, and codes are
+ * rounded to nearest even, so a value is off by at most half a step: 1 / 127.5
+ * of its block's largest magnitude, or 2^-127 where that is more.  A block
+ * that holds an infinity or a NaN has the exponent byte 255 and reads back as
+ * NaN throughout.  The exponent byte of a finite block is at most 248: beyond
+ * 127.5 * 2^121 (3.39e38) codes saturate at 127, up to one step off.
+ */
+#define SSD_PACK8_BLOCK 64
+typedef struct {
+    int8_t *codes; /* [rows, cols]                                    */
+    uint8_t *exps; /* [rows, ceil(cols / SSD_PACK8_BLOCK)]            */
+} ssd_packed8_t;
+
+/*
+ * ssd_pack8 / ssd_unpack8 -- an activation [rows, cols] of `dtype` (an
+ * ssd_dtype_t) into its 8-bit checkpoint, and back.  Unpacking is exact in
+ * either type (a code has 7 bits and a sign).  rows, cols >= 1
+ * (SSD_ERR_INVALID_DIM), at most 2^33 blocks (SSD_ERR_UNSUPPORTED).  One launch.
+ */
+SSD_API ssd_status_t ssd_pack8(int64_t rows, int64_t cols, int dtype, const void *x,
+                               const ssd_packed8_t *packed, void *stream);
+SSD_API ssd_status_t ssd_unpack8(int64_t rows, int64_t cols, int dtype, const ssd_packed8_t *packed,
+                                 void *out, void *stream);
+
+/*
+ * ssd_glr_forward -- the recurrence over whole sequences.
+ *
+ *   cu_seqlens  NULL: every row of the batch is one sequence.  Else a HOST
+ *               array of nseq + 1 offsets (batch must be 1): cu_seqlens[0] = 0,
+ *               non-decreasing, cu_seqlens[nseq] = seqlen (empty sequences
+ *               allowed), read during the call only: the sequences packed
+ *               along the row, each from its own initial state
+ *   x, r, i     [B, T, C] dtype: the input and the pre-activations of the
+ *               recurrence gate and of the input gate
+ *   A           [C] fp32
+ *   init_state  [S, C] fp32 (S sequences: batch, or nseq), or NULL for zeros
+ *   y_out       [B, T, C] dtype; must not alias any input
+ *   final_state_out  [S, C] fp32 or NULL; it must not overlap init_state
+ *               (an empty sequence's final state is its initial state)
+ *   chunk_states_out  fp32 [ssd_glr_chunk_rows, C] or NULL: the state entering
+ *               every SSD_GLR_CHUNK tokens of every sequence, in order, as
+ *               ssd_glr_backward takes it
+ *   packed_out  NULL, or three ssd_packed8_t that receive the 8-bit
+ *               checkpoints of x, r and i (rows = B T, cols = C)
+ * One kernel per 160 sequences (one for any batch); scratch for the hand-off
+ * between tiles (about 0.1 byte a value) is allocated stream-ordered on
+ * `stream` from the library's workspace pool and released to it before
+ * return.  Accuracy against the fp64 recurrence: max|h - h_ref| / max|h_ref|
+ * <= 1e-5 for states and SSD_F32, <= 2^-8 for y in SSD_BF16.
+ */
+SSD_API ssd_status_t ssd_glr_forward(const ssd_glr_dims_t *dims, const int64_t *cu_seqlens, int64_t nseq,
+                                     const void *x, const void *r, const void *i, const float *A,
+                                     const float *init_state, void *y_out, float *final_state_out,
+                                     float *chunk_states_out, const ssd_packed8_t *packed_out, void *stream);
+
+/* Rows of chunk_states_out: sum over sequences of ceil(length / SSD_GLR_CHUNK)
+ * (0 if the arguments are invalid). */
+SSD_API int64_t ssd_glr_chunk_rows(const ssd_glr_dims_t *dims, const int64_t *cu_seqlens, int64_t nseq);
+
+/*
+ * ssd_glr_backward -- the gradients of a scalar loss through ssd_glr_forward:
+ * with G_t = dL/dh_t = dy_t + a_{t+1} G_{t+1} (+ dfinal at a sequence's last
+ * token),
+ *   dx_t = G_t m_t s(i_t),  di_t = G_t m_t x_t s(i_t) (1 - s(i_t)),
+ *   dl_t = G_t (a_t h_{t-1} - a_t^2 s(i_t) x_t / m_t),
+ *   dr_t = dl_t l_t (1 - s(r_t)),  dA_c = sum dl_t s(r_t),  dinit = a_0 G_0.
+ * The root's derivative is taken as 0 where m_t = 0 (a gate that is closed
+ * altogether).
+ *
+ *   x, r, i     as for the forward pass, or all three NULL with `packed`:
+ *               three 8-bit checkpoints of them, read in their place
+ *   chunk_states  as ssd_glr_forward wrote them: the states inside a chunk are
+ *               computed again from the one entering it and from x, r, i as
+ *               given here
+ *   dy [B,T,C] dtype; dfinal_state [S, C] fp32 or NULL (zero)
+ *   dx, dr, di [B,T,C] dtype (must not alias any input); dA [C] fp32;
+ *   dinit_state [S, C] fp32 or NULL (an empty sequence's is its dfinal)
+ * Scratch as for the forward pass.  dA is summed in a fixed order.
+ */
+SSD_API ssd_status_t ssd_glr_backward(const ssd_glr_dims_t *dims, const int64_t *cu_seqlens, int64_t nseq,
+                                      const void *x, const void *r, const void *i, const ssd_packed8_t *packed,
+                                      const float *A, const float *chunk_states, const void *dy,
+                                      const float *dfinal_state, void *dx, void *dr, void *di, float *dA,
+                                      float *dinit_state, void *stream);
+
+/*
+ * ssd_glr_step -- one token of the recurrence for every row: the decode step
+ * on a resident state.  dims->seqlen must be 1; x_t, r_t, i_t, y_t [B, C]
+ * dtype; state [B, C] fp32, read and overwritten with the new state.  One
+ * launch, no allocation.
+ */
+SSD_API ssd_status_t ssd_glr_step(const ssd_glr_dims_t *dims, const void *x_t, const void *r_t, const void *i_t,
+                                  const float *A, float *state, void *y_t, void *stream);
+
+/*
+ * ssd_norm_rotate -- RMSNorm of every group's B and C over its dstate values
+ * and the position rotation, in one pass before the scan.  In the scan's dual
+ * form (L o C B^T) X the rows of C are the queries and the rows of B the keys,
+ * so this is their norm for each head with the rotation.  Per token and group, for
+ * v = B or C with its weight w:
+ *
+ *     n_j = w_j v_j / sqrt(mean_k v_k^2 + eps)
+ *     (o_p, o_q) = (n_p cos - n_q sin, n_p sin + n_q cos),  angle = pos * inv_freq_j
+ *
+ * for the pairs j < rotary / 2: (p, q) = (j, j + rotary / 2), or (2j, 2j + 1)
+ * with `interleaved`; values from `rotary` on are normed only.  The angle is
+ * formed in 64 bits (positions may be far), once a token for all groups.
+ *
+ *   Bm, Cm      [B, T, G, N] dtype; a token's G * N values are contiguous, the
+ *               strides between tokens and between batch rows are given (in
+ *               elements), so slices of a projection's rows are taken as they are
+ *   positions   [B, T] int64 (any value up to 2^53 in magnitude)
+ *   inv_freq    [rotary / 2] fp32 (may be NULL when rotary is 0)
+ *   weight_B, weight_C  [N] fp32, or NULL for ones
+ *   B_out, C_out  [B, T, G, N] dtype, contiguous; must not alias the inputs
+ * 1 <= dstate <= 256, rotary even and 0 <= rotary <= dstate, eps > 0 (else
+ * SSD_ERR_INVALID_DIM, or SSD_ERR_UNSUPPORTED for dstate > 256 or
+ * batch * seqlen >= 2^31).  Pointers into Bm and Cm need the alignment of their
+ * element type only.  One launch.
+ */
+typedef struct {
+    int64_t batch, seqlen, ngroups, dstate;
+    int64_t rotary;
+    int64_t B_batch_stride, B_token_stride;
+    int64_t C_batch_stride, C_token_stride;
+    int32_t dtype; /* ssd_dtype_t */
+    int32_t interleaved;
+    float eps;
+    int32_t reserved; /* must be 0 */
+} ssd_rotate_dims_t;
+
+SSD_API ssd_status_t ssd_norm_rotate(const ssd_rotate_dims_t *dims, const void *Bm, const void *Cm,
+                                     const int64_t *positions, const float *inv_freq, const float *weight_B,
+                                     const float *weight_C, void *B_out, void *C_out, void *stream);
+
+/*
+ * ssd_norm_rotate_backward -- its gradients: dB_out, dC_out [B, T, G, N] dtype,
+ * contiguous, are the cotangents of B_out and C_out; Bm, Cm as above.  With dz
+ * the cotangent rotated back and xh = v / sqrt(mean v^2 + eps):
+ *   dw = sum over tokens and groups of dz xh,   d = dz w,
+ *   dv = (d - xh mean(d xh)) / sqrt(mean v^2 + eps).
+ * dB, dC [B, T, G, N] dtype, contiguous (must not alias the inputs);
+ * dweight_B, dweight_C [N] fp32 or NULL (not computed), summed in a fixed
+ * order through stream-ordered scratch of the library's pool.
+ */
+SSD_API ssd_status_t ssd_norm_rotate_backward(const ssd_rotate_dims_t *dims, const void *dB_out,
+                                              const void *dC_out, const void *Bm, const void *Cm,
+                                              const int64_t *positions, const float *inv_freq,
+                                              const float *weight_B, const float *weight_C, void *dB, void *dC,
+                                              float *dweight_B, float *dweight_C, void *stream);
+
 /* Bytes of workspace one call needs (0 if the arguments are invalid). */
 SSD_API size_t ssd_workspace_bytes(const ssd_dims_t *dims, int chunk_len);
 

@@ -26,8 +26,11 @@ import os
 import numpy as np
 
 from . import build as _build
+from . import operators
+from .operators import glr, glr_grad, norm_rotate, norm_rotate_grad, pack8, unpack8
 
-__all__ = ["ssd_recurrent", "ssd_quadratic", "ssd_chunked", "ssd_step", "default_threads",
+__all__ = ["operators", *operators.__all__,
+           "ssd_recurrent", "ssd_quadratic", "ssd_chunked", "ssd_step", "default_threads",
            "dt_transform", "gated_rmsnorm", "ssd_block", "ssd_recurrent_grad"]
 
 

@@ -23,7 +23,9 @@ STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL_ARG", 2: "SSD_ERR_INVALID_DIM", 3: "SSD_
 EXPORTS = ("ssd_forward", "ssd_forward_ws", "ssd_forward_stage", "ssd_workspace_bytes",
            "ssd_workspace_layout", "ssd_device_status", "ssd_status_string", "ssd_version",
            "ssd_forward_static", "ssd_step", "ssd_forward_block", "ssd_block_workspace_bytes",
-           "ssd_forward_varlen", "ssd_varlen_workspace_bytes", "ssd_backward", "ssd_workspace_trim")
+           "ssd_forward_varlen", "ssd_varlen_workspace_bytes", "ssd_backward", "ssd_workspace_trim",
+           "ssd_glr_forward", "ssd_glr_backward", "ssd_glr_step", "ssd_glr_chunk_rows", "ssd_pack8", "ssd_unpack8",
+           "ssd_norm_rotate", "ssd_norm_rotate_backward")
 STAGES = ("ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan")
 
 
@@ -56,6 +58,25 @@ class BlockOpts(ctypes.Structure):
                 ("norm_apply", ctypes.c_int32), ("z", ctypes.c_void_p),
                 ("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float),
                 ("reserved0", ctypes.c_int32), ("rstd_out", ctypes.c_void_p)]
+
+
+class GlrDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class RotateDims(ctypes.Structure):
+    """ssd_rotate_dims_t: sizes and strides of a norm and rotation of B and C."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("rotary", ctypes.c_int64),
+                ("B_batch_stride", ctypes.c_int64), ("B_token_stride", ctypes.c_int64),
+                ("C_batch_stride", ctypes.c_int64), ("C_token_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class _Packed8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("exps", ctypes.c_void_p)]
 
 
 class SSDError(RuntimeError):
@@ -119,6 +140,20 @@ def load():
     lib.ssd_version.restype = ctypes.c_char_p
     lib.ssd_workspace_trim.argtypes = []
     lib.ssd_workspace_trim.restype = ctypes.c_int
+    i64, packed_p = ctypes.c_int64, ctypes.POINTER(_Packed8)
+    glr_p, rot_p = ctypes.POINTER(GlrDims), ctypes.POINTER(RotateDims)
+    lib.ssd_glr_forward.argtypes = [glr_p, vp, i64, vp, vp, vp, fp, fp, vp, fp, fp, packed_p, vp]
+    lib.ssd_glr_backward.argtypes = [glr_p, vp, i64, vp, vp, vp, packed_p, fp, fp, vp, fp, vp, vp, vp, fp, fp, vp]
+    lib.ssd_glr_step.argtypes = [glr_p, vp, vp, vp, fp, fp, vp, vp]
+    lib.ssd_glr_chunk_rows.argtypes = [glr_p, vp, i64]
+    lib.ssd_glr_chunk_rows.restype = i64
+    lib.ssd_pack8.argtypes = [i64, i64, ctypes.c_int, vp, packed_p, vp]
+    lib.ssd_unpack8.argtypes = [i64, i64, ctypes.c_int, packed_p, vp, vp]
+    lib.ssd_norm_rotate.argtypes = [rot_p, vp, vp, vp, fp, fp, fp, vp, vp, vp]
+    lib.ssd_norm_rotate_backward.argtypes = [rot_p, vp, vp, vp, vp, vp, fp, fp, fp, vp, vp, fp, fp, vp]
+    for f in (lib.ssd_glr_forward, lib.ssd_glr_backward, lib.ssd_glr_step, lib.ssd_pack8, lib.ssd_unpack8,
+              lib.ssd_norm_rotate, lib.ssd_norm_rotate_backward):
+        f.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -420,6 +455,313 @@ def step(state, x, dt, A, B, C, D=None, out=None, stream=None):
                              _ptr(state), _ptr(y), ctypes.c_void_p(stream))
     _check(st)
     return y
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence, 8-bit checkpoints, norm and rotation of B and C
+# ---------------------------------------------------------------------------
+GLR_CHUNK = 64    # SSD_GLR_CHUNK in include/ssd.h
+PACK8_BLOCK = 64  # SSD_PACK8_BLOCK in include/ssd.h
+_CODE = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+
+
+def _same(name, t, like, shape=None, dtype=None):
+    """Refuses a tensor that is not contiguous on `like`'s device with the shape and dtype given (`like`'s)."""
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.dtype != (dtype or like.dtype):
+        raise ValueError(f"{name} must be {dtype or like.dtype}")
+    if t.shape != (like.shape if shape is None else shape):
+        raise ValueError(f"{name} must be {tuple(like.shape if shape is None else shape)}, is {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _storage(name, x):
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _CODE.get(x.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return code
+
+
+class _Launch:
+    """The device and stream of one call.  With a stream other than the current
+    one the outputs are allocated for it, so that memory which the current
+    stream still uses is not taken."""
+
+    def __init__(self, dev, stream):
+        self.stack = []
+        if torch.cuda.current_device() != dev.index:
+            self.stack.append(torch.cuda.device(dev))
+        current = torch._C._cuda_getCurrentRawStream(dev.index)
+        self.stream = current if stream is None else int(getattr(stream, "cuda_stream", stream))
+        if self.stream != current:
+            self.stack.append(torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=dev)))
+
+    def __enter__(self):
+        for c in self.stack:
+            c.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+        return False
+
+
+class Packed8:
+    """An activation [..., channels] in 8 bits (``pack8``): ``codes`` int8 of its
+    shape and ``exps`` uint8 [..., ceil(channels / 64)], one power-of-two step a
+    block of 64 values."""
+    __slots__ = ("codes", "exps")
+
+    def __init__(self, codes, exps):
+        self.codes, self.exps = codes, exps
+
+    @classmethod
+    def empty(cls, shape, device):
+        return cls(torch.empty(shape, dtype=torch.int8, device=device),
+                   torch.empty((*shape[:-1], -(-shape[-1] // PACK8_BLOCK)), dtype=torch.uint8, device=device))
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    def _c(self):
+        return _Packed8(self.codes.data_ptr(), self.exps.data_ptr())
+
+
+def _check_packed(name, p, like=None, shape=None):
+    if not isinstance(p, Packed8):
+        raise ValueError(f"{name} must be a Packed8")
+    if not p.codes.is_cuda or p.codes.dim() < 1:
+        raise ValueError(f"{name} must hold CUDA tensors")
+    _same(f"{name}.codes", p.codes, p.codes if like is None else like, shape or p.codes.shape, torch.int8)
+    want = (*p.codes.shape[:-1], -(-p.codes.shape[-1] // PACK8_BLOCK))
+    _same(f"{name}.exps", p.exps, p.codes, want, torch.uint8)
+
+
+def pack8(x, stream=None):
+    """``x`` [..., channels] (float32 or bfloat16) as an 8-bit checkpoint: one
+    signed byte a value and one power-of-two step for every 64 values of a row,
+    off by at most 1/127.5 of the largest magnitude among them."""
+    code = _storage("x", x)
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError("x must be contiguous with at least one dimension")
+    cols = x.shape[-1]
+    with _Launch(x.device, stream) as st:
+        p = Packed8.empty(x.shape, x.device)
+        c = p._c()
+        _check(load().ssd_pack8(x.numel() // cols if cols else 0, cols, code, x.data_ptr(), ctypes.byref(c), st))
+    return p
+
+
+def unpack8(packed, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of a checkpoint in float32 or bfloat16 (exact in either)."""
+    _check_packed("packed", packed)
+    if out is not None:
+        _same("out", out, packed.codes, packed.shape, dtype)
+    if dtype not in _CODE:
+        raise ValueError("dtype must be float32 or bfloat16")
+    cols = packed.shape[-1]
+    with _Launch(packed.codes.device, stream) as st:
+        out = torch.empty(packed.shape, dtype=dtype, device=packed.codes.device) if out is None else out
+        c = packed._c()
+        _check(load().ssd_unpack8(packed.codes.numel() // cols if cols else 0, cols, _CODE[dtype], ctypes.byref(c),
+                                  out.data_ptr(), st))
+    return out
+
+
+class GlrSaved:
+    """What ``glr_forward`` keeps for ``glr_backward``: the inputs, or their 8-bit
+    checkpoints, and the state entering every 64 tokens of every sequence."""
+    __slots__ = ("x", "r", "i", "A", "chunk_states", "cu", "rows")
+
+    def __init__(self, x, r, i, A, chunk_states, cu, rows):
+        self.x, self.r, self.i, self.A, self.chunk_states, self.cu, self.rows = x, r, i, A, chunk_states, cu, rows
+
+
+def _glr_dims(x):
+    code = _storage("x", x)
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, channels]")
+    return GlrDims(x.shape[0], x.shape[1], x.shape[2], code, 0)
+
+
+def glr_forward(x, r, i, A, init_state=None, cu_seqlens=None, return_final_state=False, save=None, out=None,
+                stream=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(i_t) x_t with
+    a_t = exp(A s(r_t)), s the logistic function, through ``ssd_glr_forward``.
+
+    x, r, i [B, T, C] (float32 or bfloat16, one dtype); A [C] float32, at most 0;
+    ``cu_seqlens`` (host: a list, a numpy array or a CPU tensor; B must be 1)
+    holds nseq + 1 offsets of sequences packed along T; init_state and the final
+    state are [B or nseq, C] float32.  ``save`` keeps what ``glr_backward`` needs:
+    "inputs" refers to x, r and i themselves, "packed8" writes 8-bit
+    checkpoints of them in the same pass.  Returns y plus, as asked, the final
+    state and the saved (in that order)."""
+    dims = _glr_dims(x)
+    _same("x", x, x)
+    _same("r", r, x)
+    _same("i", i, x)
+    C = x.shape[2]
+    _same("A", A, x, (C,), torch.float32)
+    if save not in (None, "inputs", "packed8"):
+        raise ValueError('save must be None, "inputs" or "packed8"')
+    cu = None if cu_seqlens is None else _cu_array(cu_seqlens)
+    nseq = 0 if cu is None else cu.size - 1
+    rows = nseq if cu is not None else x.shape[0]
+    if init_state is not None:
+        _same("init_state", init_state, x, (rows, C), torch.float32)
+    if out is not None:
+        _same("out", out, x)
+    lib = load()
+    cu_p = None if cu is None else cu.ctypes.data
+    states = packed = final = None
+    with _Launch(x.device, stream) as st:
+        y = torch.empty_like(x) if out is None else out
+        if return_final_state:
+            final = torch.empty((rows, C), dtype=torch.float32, device=x.device)
+        if save is not None:
+            states = torch.empty((lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C), dtype=torch.float32,
+                                 device=x.device)
+            if save == "packed8":
+                packed = [Packed8.empty(x.shape, x.device) for _ in range(3)]
+        pk = None if packed is None else (_Packed8 * 3)(*(p._c() for p in packed))
+        _check(lib.ssd_glr_forward(
+            ctypes.byref(dims), cu_p, nseq, x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
+            None if init_state is None else init_state.data_ptr(), y.data_ptr(),
+            None if final is None else final.data_ptr(), None if states is None else states.data_ptr(), pk, st))
+    res = [y]
+    if return_final_state:
+        res.append(final)
+    if save is not None:
+        res.append(GlrSaved(*(packed or (x, r, i)), A, states, cu, rows))
+    return res[0] if len(res) == 1 else tuple(res)
+
+
+def glr_backward(dy, saved, dfinal_state=None, return_dinit_state=False, stream=None):
+    """Gradients of ``glr_forward`` through ``ssd_glr_backward``, from what it saved
+    and the cotangents dy [B, T, C] and dfinal_state [B or nseq, C]: a dict with
+    dx, dr, di (dy's dtype), dA, and dinit_state (None unless asked for)."""
+    if not isinstance(saved, GlrSaved):
+        raise ValueError("saved must be what glr_forward returned with save=")
+    dims = _glr_dims(dy)
+    _same("dy", dy, dy)
+    C = dy.shape[2]
+    packed = isinstance(saved.x, Packed8)
+    for name, t in (("x", saved.x), ("r", saved.r), ("i", saved.i)):
+        if packed:
+            _check_packed(f"the saved {name}", t, dy, dy.shape)
+        else:
+            _same(f"the saved {name}", t, dy)
+    _same("the saved A", saved.A, dy, (C,), torch.float32)
+    cu = saved.cu
+    nseq = 0 if cu is None else cu.size - 1
+    lib = load()
+    cu_p = None if cu is None else cu.ctypes.data
+    _same("the saved chunk_states", saved.chunk_states, dy,
+          (lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C), torch.float32)
+    if dfinal_state is not None:
+        _same("dfinal_state", dfinal_state, dy, (saved.rows, C), torch.float32)
+    with _Launch(dy.device, stream) as st:
+        dx, dr, di, dA = (torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(dy),
+                          torch.empty_like(saved.A))
+        dinit = torch.empty((saved.rows, C), dtype=torch.float32, device=dy.device) if return_dinit_state else None
+        pk = (_Packed8 * 3)(saved.x._c(), saved.r._c(), saved.i._c()) if packed else None
+        ins = (None, None, None) if packed else (saved.x.data_ptr(), saved.r.data_ptr(), saved.i.data_ptr())
+        _check(lib.ssd_glr_backward(
+            ctypes.byref(dims), cu_p, nseq, *ins, pk, saved.A.data_ptr(), saved.chunk_states.data_ptr(),
+            dy.data_ptr(), None if dfinal_state is None else dfinal_state.data_ptr(), dx.data_ptr(), dr.data_ptr(),
+            di.data_ptr(), dA.data_ptr(), None if dinit is None else dinit.data_ptr(), st))
+    return dict(dx=dx, dr=dr, di=di, dA=dA, dinit_state=dinit)
+
+
+def glr_step(state, x, r, i, A, out=None, stream=None):
+    """One token of the gated linear recurrence through ``ssd_glr_step``: ``state``
+    [B, C] float32 is updated in place and the output is returned.  x, r, i
+    [B, C] (float32 or bfloat16, one dtype); A [C] float32."""
+    code = _storage("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, channels]")
+    _same("x", x, x)
+    _same("r", r, x)
+    _same("i", i, x)
+    B, C = x.shape
+    _same("A", A, x, (C,), torch.float32)
+    _same("state", state, x, x.shape, torch.float32)
+    if out is not None:
+        _same("out", out, x)
+    dims = GlrDims(B, 1, C, code, 0)
+    with _Launch(x.device, stream) as st:
+        y = torch.empty_like(x) if out is None else out
+        _check(load().ssd_glr_step(ctypes.byref(dims), x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
+                                   state.data_ptr(), y.data_ptr(), st))
+    return y
+
+
+def _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved):
+    code = _storage("B", B)
+    if B.dim() != 4:
+        raise ValueError("B and C must be [batch, seqlen, ngroups, dstate]")
+    bsz, T, G, N = B.shape
+    for name, t in (("B", B), ("C", C)):
+        if t.device != B.device or t.dtype != B.dtype or t.shape != B.shape:
+            raise ValueError("B and C must have one shape, dtype and device")
+        s = t.stride()
+        if (N > 1 and s[3] != 1) or (G > 1 and s[2] != N):
+            raise ValueError(f"a token's values of {name} must be contiguous")
+    if positions.dtype != torch.int64:
+        raise ValueError("positions must be int64")
+    _same("positions", positions, B, (bsz, T), torch.int64)
+    _same("inv_freq", inv_freq, B, (inv_freq.numel(),), torch.float32)
+    for name, t in (("weight_B", weight_B), ("weight_C", weight_C)):
+        if t is not None:
+            _same(name, t, B, (N,), torch.float32)
+    (b0, b1), (c0, c1) = B.stride()[:2], C.stride()[:2]
+    return RotateDims(bsz, T, G, N, 2 * inv_freq.numel(), b0, b1, c0, c1, code, 1 if interleaved else 0, float(eps), 0)
+
+
+def norm_rotate(B, C, positions, inv_freq, weight_B=None, weight_C=None, eps=1e-5, interleaved=False, stream=None):
+    """RMSNorm over dstate of every group's B and C and the position rotation,
+    through ``ssd_norm_rotate``: what the scan takes as its B and C.
+
+    B, C [batch, seqlen, ngroups, dstate] (float32 or bfloat16; slices of a
+    projection's rows are taken as they are); positions [batch, seqlen] int64;
+    inv_freq [rotary / 2] float32, rotary at most dstate; weights [dstate]
+    float32 or None.  Pairs are (j, j + rotary / 2), or neighbours with
+    ``interleaved``.  Returns (B, C), contiguous."""
+    dims = _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved)
+    with _Launch(B.device, stream) as st:
+        Bo, Co = (torch.empty(B.shape, dtype=B.dtype, device=B.device) for _ in range(2))
+        _check(load().ssd_norm_rotate(
+            ctypes.byref(dims), B.data_ptr(), C.data_ptr(), positions.data_ptr(),
+            inv_freq.data_ptr() if dims.rotary else None, None if weight_B is None else weight_B.data_ptr(),
+            None if weight_C is None else weight_C.data_ptr(), Bo.data_ptr(), Co.data_ptr(), st))
+    return Bo, Co
+
+
+def norm_rotate_backward(dB_out, dC_out, B, C, positions, inv_freq, weight_B=None, weight_C=None, eps=1e-5,
+                         interleaved=False, stream=None):
+    """Gradients of ``norm_rotate`` through ``ssd_norm_rotate_backward``, from the
+    cotangents of its outputs and its inputs: a dict with dB, dC (contiguous),
+    dweight_B and dweight_C (None without that weight)."""
+    dims = _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved)
+    _same("dB_out", dB_out, B)
+    _same("dC_out", dC_out, B)
+    with _Launch(B.device, stream) as st:
+        dB, dC = torch.empty_like(dB_out), torch.empty_like(dC_out)
+        dwB = None if weight_B is None else torch.empty_like(weight_B)
+        dwC = None if weight_C is None else torch.empty_like(weight_C)
+        _check(load().ssd_norm_rotate_backward(
+            ctypes.byref(dims), dB_out.data_ptr(), dC_out.data_ptr(), B.data_ptr(), C.data_ptr(),
+            positions.data_ptr(), inv_freq.data_ptr() if dims.rotary else None,
+            None if weight_B is None else weight_B.data_ptr(), None if weight_C is None else weight_C.data_ptr(),
+            dB.data_ptr(), dC.data_ptr(), None if dwB is None else dwB.data_ptr(),
+            None if dwC is None else dwC.data_ptr(), st))
+    return dict(dB=dB, dC=dC, dweight_B=dwB, dweight_C=dwC)
 
 
 def device_status(device=None) -> int:

@@ -1,0 +1,44 @@
+// pack8.cuh -- the 8-bit activation checkpoint: blocks of 64 values along a row
+// share one power-of-two step 2^(e - 127), e the block's exponent byte, and each
+// value is a signed byte of steps.
+//
+// With a power of two, value / step and code * step are exact, so a value read
+// back depends on nothing but the block's largest magnitude and the rounding
+// to the nearest code (ties to even), and is a bf16 number (7 bits and a sign).
+// A step of max / 127 would use up to one more bit of the code, for a division
+// a value and four bytes a block in place of one.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+constexpr int kPackBlock = 64;
+
+// Exponent byte of a block from the bits of its largest magnitude (sign
+// cleared; a NaN's bits are above infinity's): the smallest e >= 1 with
+// max < 127.5 * 2^(e - 127), so that the largest code rounds to at most 127.
+// 127.5 = 1.9921875 * 2^6: the mantissa decides between E - 6 and E - 5.  At most
+// 248 (64 steps of the next one are past the largest float): there alone codes
+// saturate.  255 for a block with an infinity or a NaN.
+__device__ __forceinline__ uint32_t pack8_exp(uint32_t maxbits) {
+    const uint32_t E = maxbits >> 23;
+    const uint32_t up = (maxbits & 0x7fffffu) >= 0x7f0000u ? 5u : 6u;
+    const uint32_t e = E > up ? E - up : 1u;
+    return E == 255u ? 255u : min(e, 248u);
+}
+// 1 / step as a float (0 for the byte 255: every code of such a block is 0)
+__device__ __forceinline__ float pack8_inv(uint32_t e) {
+    return __uint_as_float(e == 255u ? 0u : (254u - e) << 23);
+}
+// step as a float; infinity for the byte 255, so that its codes, all 0, read
+// back as NaN
+__device__ __forceinline__ float pack8_step(uint32_t e) { return __uint_as_float(e << 23); }
+// The code of v, -127 .. 127.  v * inv is exact, but for values far below the
+// smallest step.  An infinity or NaN times 0 is NaN, which converts to 0.
+__device__ __forceinline__ int pack8_code(float v, float inv) {
+    return min(max(__float2int_rn(v * inv), -127), 127);
+}
+
+}  // namespace ssd

@@ -13,6 +13,7 @@
 
 #include "../../include/ssd.h"
 #include "common.cuh"
+#include "glr.h"
 #include "kernels.h"
 
 // Device word set by tensor-core kernels whose bounded waits expired.
@@ -25,6 +26,10 @@ using ssd::Dims;
 constexpr int kMaxDevices = 64;
 unsigned int *g_err_ptr[kMaxDevices];  // per-device address of g_ssd_device_error
 std::once_flag g_err_once[kMaxDevices];
+
+}  // namespace
+
+namespace ssd {
 
 // Address of the error word on the current device (NULL if unavailable).
 unsigned int *device_error_word() {
@@ -42,6 +47,12 @@ unsigned int *device_error_word() {
     });
     return g_err_ptr[dev];
 }
+
+}  // namespace ssd
+
+namespace {
+
+using ssd::device_error_word;
 
 // Workspace memory of the entry points that allocate their own: a stream-
 // ordered pool per device, private to the library, that keeps what it has
@@ -74,6 +85,10 @@ cudaMemPool_t workspace_pool(int dev) {
     return g_pool[dev];
 }
 
+}  // namespace
+
+namespace ssd {
+
 cudaError_t workspace_alloc(void **p, size_t bytes, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -83,6 +98,12 @@ cudaError_t workspace_alloc(void **p, size_t bytes, cudaStream_t st) {
     cudaMemPool_t pool = workspace_pool(dev);
     return pool ? cudaMallocFromPoolAsync(p, bytes, pool, st) : cudaMallocAsync(p, bytes, st);
 }
+
+}  // namespace ssd
+
+namespace {
+
+using ssd::workspace_alloc;
 
 constexpr size_t kAlign = 256;
 // the backward's per-row kernels keep one factor per head in shared memory
