@@ -29,10 +29,10 @@ struct GlrShape {
 };
 
 // Scratch of one launch: the hand-off of the states between the tiles of a
-// chain.  With one chunk a sequence there is none and every pointer is null.
+// chain, all ones at the start.  With one chunk a sequence there is none and
+// every pointer is null.
 struct GlrScratch {
-    unsigned int *ticket;  // next tile; 0 at the start
-    unsigned int *flags;   // [tiles] 0, 1 (sums published), 2 (state published)
+    unsigned int *ticket;  // the last tile taken
     float4 *sums;          // [tiles][32] products and sums of two channels a lane
     float2 *state;         // [tiles][32] the state that leaves the tile
 };

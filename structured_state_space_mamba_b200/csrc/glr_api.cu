@@ -91,23 +91,20 @@ struct Groups {
     }
 };
 
-// Scratch of the launches inside one allocation: the tickets and flags (zeroed)
-// of all of them first, then their sums and states.
+// Scratch of the launches, one after another inside an allocation.
 struct ScratchPlan {
-    size_t zero = 0, data = 0;  // bytes of either part, so far
+    size_t bytes = 0;  // so far
     static size_t tiles(const GlrShape &s) { return size_t(s.nct) * s.nc * (s.nseq ? 1 : s.batch); }
-    // adds a launch; its scratch, when `buf` (whose first part has `zeros` bytes) is given
-    GlrScratch add(const GlrShape &s, bool linked, char *buf = nullptr, size_t zeros = 0) {
+    // adds a launch; its scratch, when the allocation is there
+    GlrScratch add(const GlrShape &s, bool linked, char *buf = nullptr) {
         GlrScratch w = {};
         if (!linked) return w;
         if (buf) {
-            w.ticket = reinterpret_cast<unsigned int *>(buf + zero);
-            w.flags = w.ticket + 64;
-            w.sums = reinterpret_cast<float4 *>(buf + zeros + data);
+            w.ticket = reinterpret_cast<unsigned int *>(buf + bytes);
+            w.sums = reinterpret_cast<float4 *>(buf + bytes + kAlign);
             w.state = reinterpret_cast<float2 *>(w.sums + tiles(s) * 32);
         }
-        zero += align_up(4 * (tiles(s) + 64));
-        data += align_up(tiles(s) * 32 * (sizeof(float4) + sizeof(float2)));
+        bytes += kAlign + align_up(tiles(s) * 32 * (sizeof(float4) + sizeof(float2)));
         return w;
     }
 };
@@ -202,18 +199,17 @@ ssd_status_t ssd_glr_forward(const ssd_glr_dims_t *dims, const int64_t *cu_seqle
     ScratchPlan plan;
     for (Groups g{*dims, cu_seqlens, nseq}; g.next(shape, linked);) plan.add(shape, linked);
     char *buf = nullptr;
-    const size_t bytes = plan.zero + plan.data;
-    if (bytes) {
-        if (ssd::workspace_alloc(reinterpret_cast<void **>(&buf), bytes, st) != cudaSuccess) {
+    if (plan.bytes) {
+        if (ssd::workspace_alloc(reinterpret_cast<void **>(&buf), plan.bytes, st) != cudaSuccess) {
             cudaGetLastError();
             return SSD_ERR_WORKSPACE;
         }
-        if (cudaMemsetAsync(buf, 0, plan.zero, st) != cudaSuccess) s = SSD_ERR_CUDA;
+        if (cudaMemsetAsync(buf, 0xff, plan.bytes, st) != cudaSuccess) s = SSD_ERR_CUDA;
     }
     ScratchPlan used;
     for (Groups g{*dims, cu_seqlens, nseq}; s == SSD_OK && g.next(shape, linked);)
         if (ssd::launch_glr_forward(shape, bf16, x, r, i, A, init_state, y_out, final_state_out, chunk_states_out,
-                                    packed_out ? &pk : nullptr, used.add(shape, linked, buf, plan.zero), err,
+                                    packed_out ? &pk : nullptr, used.add(shape, linked, buf), err,
                                     st) != cudaSuccess)
             s = SSD_ERR_CUDA;
     if (s == SSD_OK) s = copy_empty(cu_seqlens, nseq, dims->channels, init_state, final_state_out, st);
@@ -249,17 +245,17 @@ ssd_status_t ssd_glr_backward(const ssd_glr_dims_t *dims, const int64_t *cu_seql
     ScratchPlan plan;
     for (Groups g{*dims, cu_seqlens, nseq}; g.next(shape, linked);) plan.add(shape, linked);
     char *buf = nullptr;
-    const size_t part_off = plan.zero + plan.data, bytes = part_off + size_t(chunks) * C * sizeof(float);
+    const size_t part_off = plan.bytes, bytes = part_off + size_t(chunks) * C * sizeof(float);
     if (ssd::workspace_alloc(reinterpret_cast<void **>(&buf), bytes, st) != cudaSuccess) {
         cudaGetLastError();
         return SSD_ERR_WORKSPACE;
     }
     float *part = reinterpret_cast<float *>(buf + part_off);
-    if (plan.zero && cudaMemsetAsync(buf, 0, plan.zero, st) != cudaSuccess) s = SSD_ERR_CUDA;
+    if (plan.bytes && cudaMemsetAsync(buf, 0xff, plan.bytes, st) != cudaSuccess) s = SSD_ERR_CUDA;
     ScratchPlan used;
     for (Groups g{*dims, cu_seqlens, nseq}; s == SSD_OK && g.next(shape, linked);)
         if (ssd::launch_glr_backward(shape, bf16, x, r, i, packed ? &pk : nullptr, A, chunk_states, dy, dfinal_state,
-                                     dx, dr, di, dinit_state, part, used.add(shape, linked, buf, plan.zero), err,
+                                     dx, dr, di, dinit_state, part, used.add(shape, linked, buf), err,
                                      st) != cudaSuccess)
             s = SSD_ERR_CUDA;
     if (s == SSD_OK && ssd::launch_row_sum(part, chunks, C, dA, st) != cudaSuccess) s = SSD_ERR_CUDA;

@@ -11,7 +11,7 @@
 // channels is read once, its gates are formed in registers, and the tiles of
 // one chain (a sequence's chunks for 64 channels) hand the state on through
 // global memory in the same launch.  A tile publishes its (product, sum) as
-// soon as it has them; a later tile looks back over at most 32 predecessors
+// soon as it has them; a later tile looks back over at most 16 predecessors
 // to the nearest one whose outgoing state is known and applies the sums in
 // between in their order, so the bits do not depend on how far it looked.
 // Tiles are taken by ticket, chunk by chunk over all chains: a tile only ever
@@ -24,13 +24,14 @@
 #include "glr.h"
 #include "pack8.cuh"
 #include "tc_common.cuh"
+#include "tma_host.h"
 
 namespace ssd {
 
 namespace {
 
 // ---------------------------------------------------------------------------
-// gates
+// gates: two channels at a time, in the packed fp32 operations
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float ex2(float v) {
     float r;
@@ -47,80 +48,96 @@ __device__ __forceinline__ float rsq(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float root(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 // the larger of the two, NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 struct Gate {
-    float sr, si;  // s(r), s(i)
-    float cr, ci;  // 1 - s(r), 1 - s(i)
-    float l, e1;   // log decay, decay - 1
-    float v;       // 1 - decay^2
+    float2 sr, si;  // s(r), s(i)
+    float2 er, ei;  // e^-r, e^-i: 1 - s(r) = er * sr
+    float2 l, e1;   // log decay, decay - 1
+    float2 w;       // decay^2 - 1
 };
 
 // e^l - 1 for l <= 0: the Taylor sum to l^7 from -1/2 up (the next term is below
 // 2^-22 of the result there), the exponential below (where its error is no
 // longer magnified by the difference).
-__device__ __forceinline__ float decay_minus_1(float l) {
-    float p = fmaf(l, 1.f / 5040.f, 1.f / 720.f);
-    p = fmaf(l, p, 1.f / 120.f);
-    p = fmaf(l, p, 1.f / 24.f);
-    p = fmaf(l, p, 1.f / 6.f);
-    p = fmaf(l, p, 0.5f);
-    p = fmaf(l, p, 1.f);
-    p *= l;
-    if (l < -0.5f) p = ex2(l * 1.4426950408889634f) - 1.f;
+__device__ __forceinline__ float2 decay_minus_1(float2 l) {
+    float2 p = fma(l, both(1.f / 5040.f), both(1.f / 720.f));
+    p = fma(l, p, both(1.f / 120.f));
+    p = fma(l, p, both(1.f / 24.f));
+    p = fma(l, p, both(1.f / 6.f));
+    p = fma(l, p, both(0.5f));
+    p = fma(l, p, both(1.f));
+    p = mul(p, l);
+    if (fminf(l.x, l.y) < -0.5f) {
+        if (l.x < -0.5f) p.x = ex2(l.x * 1.4426950408889634f) - 1.f;
+        if (l.y < -0.5f) p.y = ex2(l.y * 1.4426950408889634f) - 1.f;
+    }
     return p;
 }
 
 // One reciprocal serves both sigmoids; the arguments are held at -43 so that
 // the product of the two denominators stays finite (s(-43) = 2e-19).
-__device__ __forceinline__ Gate gate(float r, float i, float A) {
+__device__ __forceinline__ Gate gate(float2 r, float2 i, float2 A) {
     Gate g;
-    const float er = ex2(max_nan(r, -43.f) * -1.4426950408889634f);
-    const float ei = ex2(max_nan(i, -43.f) * -1.4426950408889634f);
-    const float q = rcp((1.f + er) * (1.f + ei));
-    g.sr = (1.f + ei) * q;
-    g.si = (1.f + er) * q;
-    g.cr = er * g.sr;
-    g.ci = ei * g.si;
-    g.l = A * g.sr;
+    const float2 k = both(-1.4426950408889634f);
+    const float2 tr = mul(make_float2(max_nan(r.x, -43.f), max_nan(r.y, -43.f)), k);
+    const float2 ti = mul(make_float2(max_nan(i.x, -43.f), max_nan(i.y, -43.f)), k);
+    g.er = make_float2(ex2(tr.x), ex2(tr.y));
+    g.ei = make_float2(ex2(ti.x), ex2(ti.y));
+    const float2 dr = add(g.er, both(1.f)), di = add(g.ei, both(1.f));
+    const float2 d = mul(dr, di), q = make_float2(rcp(d.x), rcp(d.y));
+    g.sr = mul(di, q);
+    g.si = mul(dr, q);
+    g.l = mul(A, g.sr);
     g.e1 = decay_minus_1(g.l);
-    g.v = -g.e1 * (2.f + g.e1);
+    g.w = mul(g.e1, add(g.e1, both(2.f)));
     return g;
 }
-// 1 / sqrt(v), 0 for 0
-__device__ __forceinline__ float inv_root(float v) { return v == 0.f ? 0.f : rsq(v); }
+// what a token brings in: sqrt(1 - a^2) s(i) x
+__device__ __forceinline__ float2 income(const Gate &g, float2 x) {
+    return mul(mul(make_float2(root(-g.w.x), root(-g.w.y)), g.si), x);
+}
+// 1 / sqrt(-w), 0 for 0
+__device__ __forceinline__ float inv_root(float w) { return w == 0.f ? 0.f : rsq(-w); }
+// h + e1 h + u
+__device__ __forceinline__ float2 advance(float2 h, float2 e1, float2 u) { return add(fma(e1, h, h), u); }
 
 // ---------------------------------------------------------------------------
 // storage: two channels a lane
 // ---------------------------------------------------------------------------
-// EVEN: the channel count is even, so a lane's pair is one aligned access and
+// VEC: rows are whole 16-byte vectors, so a lane's pair is one aligned access and
 // both channels exist or neither does.
-template <typename T, bool EVEN>
-__device__ __forceinline__ float2 load2(const T *p, bool a0, bool a1) {
-    float2 v = make_float2(0.f, 0.f);
-    if (EVEN) {
-        if (a0) {
-            if constexpr (sizeof(T) == 2) {
-                const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(p));
-                v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-            } else {
-                v = __ldg(reinterpret_cast<const float2 *>(p));
-            }
-        }
+template <typename T>
+__device__ __forceinline__ float2 unpack2(const T *p) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     } else {
-        if (a0) v.x = to_f32<T>(p[0]);
-        if (a1) v.y = to_f32<T>(p[1]);
+        return *reinterpret_cast<const float2 *>(p);
     }
-    return v;
 }
-template <typename T, bool EVEN>
+template <bool VEC>
+__device__ __forceinline__ float2 load2(const float *p, bool a0, bool a1) {
+    if (VEC) return a0 ? __ldg(reinterpret_cast<const float2 *>(p)) : make_float2(0.f, 0.f);
+    return make_float2(a0 ? p[0] : 0.f, a1 ? p[1] : 0.f);
+}
+template <typename T, bool VEC>
 __device__ __forceinline__ void store2(T *p, float2 v, bool a0, bool a1) {
-    if (EVEN) {
+    if (VEC) {
         if (a0) {
             if constexpr (sizeof(T) == 2)
                 *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
@@ -132,28 +149,32 @@ __device__ __forceinline__ void store2(T *p, float2 v, bool a0, bool a1) {
         if (a1) p[1] = from_f32<T>(v.y);
     }
 }
-template <bool EVEN>
-__device__ __forceinline__ float2 load_code2(const int8_t *p, float step, bool a0, bool a1) {
-    float2 v = make_float2(0.f, 0.f);
-    if (EVEN) {
-        if (a0) {
-            const char2 c = __ldg(reinterpret_cast<const char2 *>(p));
-            v = make_float2(float(c.x) * step, float(c.y) * step);
-        }
-    } else {
-        if (a0) v.x = float(p[0]) * step;
-        if (a1) v.y = float(p[1]) * step;
-    }
-    return v;
-}
-template <bool EVEN>
+template <bool VEC>
 __device__ __forceinline__ void store_code2(int8_t *p, int c0, int c1, bool a0, bool a1) {
-    if (EVEN) {
+    if (VEC) {
         if (a0) *reinterpret_cast<char2 *>(p) = make_char2(char(c0), char(c1));
     } else {
         if (a0) p[0] = int8_t(c0);
         if (a1) p[1] = int8_t(c1);
     }
+}
+
+// ---------------------------------------------------------------------------
+// shared memory: a ring of stages, each the raw values of one tile
+// ---------------------------------------------------------------------------
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes) {
+    const uint32_t d = tc::smem_u32(dst);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(bytes), "n"(BYTES)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -209,43 +230,83 @@ __device__ __forceinline__ Tile decode_tile(const GlrShape &s, int tile, bool re
     return t;
 }
 
-__device__ __forceinline__ unsigned int ld_acquire(const unsigned int *f) {
-    unsigned int v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
+// ---------------------------------------------------------------------------
+// the hand-off: values that are their own flags
+// ---------------------------------------------------------------------------
+// The scratch starts as all ones, a NaN that no arithmetic here produces (a
+// computed NaN is 0x7fffffff), so a word that differs from it has been written.
+// A reader looks at the words it needs themselves: no fence, no flag, one trip
+// through L2.
+constexpr uint32_t kUnset = 0xffffffffu;
+
+__device__ __forceinline__ void put_sums(const GlrScratch &ws, int tile, int lane, float2 P, float2 S) {
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(ws.sums + int64_t(tile) * 32 + lane),
+                 "f"(P.x), "f"(P.y), "f"(S.x), "f"(S.y) : "memory");
+}
+__device__ __forceinline__ void put_state(const GlrScratch &ws, int tile, int lane, float2 h) {
+    asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(ws.state + int64_t(tile) * 32 + lane),
+                 "f"(h.x), "f"(h.y) : "memory");
+}
+__device__ __forceinline__ uint32_t get_word(const void *p) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_release(unsigned int *f, unsigned int v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(f), "r"(v) : "memory");
+__device__ __forceinline__ float4 get_sums(const GlrScratch &ws, int64_t tile, int lane) {
+    float4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(ws.sums + tile * 32 + lane) : "memory");
+    return v;
 }
+__device__ __forceinline__ float2 get_state(const GlrScratch &ws, int64_t tile, int lane) {
+    float2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y)
+                 : "l"(ws.state + tile * 32 + lane) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool set(float v) { return __float_as_uint(v) != kUnset; }
+__device__ __forceinline__ bool set(float2 v) { return set(v.x) && set(v.y); }
+__device__ __forceinline__ bool set(float4 v) { return set(v.x) && set(v.y) && set(v.z) && set(v.w); }
 
-// One warp publishes a tile's sums or its outgoing state.
-__device__ __forceinline__ void publish_sums(const GlrScratch &ws, const Tile &t, float2 P, float2 S, int lane) {
-    ws.sums[int64_t(t.tile) * 32 + lane] = make_float4(P.x, P.y, S.x, S.y);
-    __syncwarp();
-    if (lane == 0) st_release(ws.flags + t.tile, 1u);
-}
-__device__ __forceinline__ void publish_state(const GlrScratch &ws, const Tile &t, float2 h, int lane) {
-    ws.state[int64_t(t.tile) * 32 + lane] = h;
-    __syncwarp();
-    if (lane == 0) st_release(ws.flags + t.tile, 2u);
-}
+constexpr int kWindow = 16;  // predecessors that a tile looks back over
+constexpr int kBatch = 4;    // sums fetched at a time
 
-// The state that enters the tile, for one warp (t.rank > 0).  Lane l watches the
-// l-th predecessor.  Gives up with the error word set after kWaitLimitNs.
+// The state that enters the tile, for one warp (t.rank > 0): the outgoing state of
+// the nearest predecessor that has published it, taken through the sums of those
+// in between, in their order.  Lanes 0 .. 15 watch the predecessors' states,
+// lanes 16 .. 31 their sums.  Gives up with the error word set after kWaitLimitNs.
 __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, int lane, float2 &h,
                                           unsigned int *err) {
-    const int window = min(t.rank, 32);
-    const unsigned int *f = ws.flags + (t.tile - int64_t(lane + 1) * t.stride);
-    int d = 0;
+    const int window = min(t.rank, kWindow), mine = lane % kWindow;
+    const int64_t watched = (t.tile - int64_t(mine + 1) * t.stride) * 32;
+    const void *f = lane < kWindow ? static_cast<const void *>(ws.state + watched)
+                                   : static_cast<const void *>(ws.sums + watched);
     uint64_t t0 = 0;
     for (uint32_t n = 0;; ++n) {
-        const unsigned int v = lane < window ? ld_acquire(f) : 0u;
-        const unsigned int done = __ballot_sync(0xffffffffu, v == 2u);
-        const unsigned int some = __ballot_sync(0xffffffffu, v != 0u);
-        if (done) {
-            d = __ffs(done) - 1;
-            const unsigned int nearer = (1u << d) - 1u;
-            if ((some & nearer) == nearer) break;
+        const uint32_t v = mine < window ? get_word(f) : kUnset;
+        const uint32_t seen = __ballot_sync(0xffffffffu, v != kUnset);
+        const uint32_t states = seen & ((1u << kWindow) - 1u), sums = seen >> kWindow;
+        if (states) {
+            const int d = __ffs(states) - 1;
+            const uint32_t nearer = (1u << d) - 1u;
+            if ((sums & nearer) == nearer) {
+                // one word of each tile has been seen; every lane checks its own
+                h = get_state(ws, t.tile - int64_t(d + 1) * t.stride, lane);
+                bool ok = set(h);
+                for (int e = d; e > 0; e -= kBatch) {
+                    float4 q[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (k < e) q[k] = get_sums(ws, t.tile - int64_t(e - k) * t.stride, lane);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (k < e) {
+                            ok = ok && set(q[k]);
+                            h = fma(make_float2(q[k].x, q[k].y), h, make_float2(q[k].z, q[k].w));
+                        }
+                }
+                if (__all_sync(0xffffffffu, ok)) return true;
+            }
         }
         if ((n & 15u) == 15u) {
             const uint64_t now = tc::global_ns();
@@ -258,21 +319,66 @@ __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, i
             }
         }
     }
-    __syncwarp();
-    h = __ldcg(ws.state + (t.tile - int64_t(d + 1) * t.stride) * 32 + lane);
-    for (int e = d - 1; e >= 0; --e) {
-        const float4 q = __ldcg(ws.sums + (t.tile - int64_t(e + 1) * t.stride) * 32 + lane);
-        h.x = fmaf(q.x, h.x, q.z);
-        h.y = fmaf(q.y, h.y, q.w);
-    }
-    return true;
 }
 
-// h + e1 h + u
-__device__ __forceinline__ float advance(float h, float e1, float u) { return fmaf(e1, h, h) + u; }
+constexpr int kWarps = 8;                     // compute warps of a tile
+constexpr int kThreads = 32 * (kWarps + 1);   // and the scan warp
+constexpr int kTok = kGlrChunk / kWarps;      // tokens of a warp
+constexpr int kWarpVals = kTok * kGlrCols;
 
-constexpr int kWarps = 16;            // warps of a tile
-constexpr int kTok = kGlrChunk / kWarps;  // tokens of a warp
+// One warp's tokens of a tile of a [tokens, C] array; zeros where there is nothing.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fill(T *dst, const T *src, const Tile &t, int C, int warp, int lane) {
+    const int c0 = t.ct * kGlrCols, ntok = t.ntok - warp * kTok;
+    const int64_t tok = t.tok + warp * kTok;
+    if (VEC) {
+        constexpr int kBytes = sizeof(T) == 1 ? 8 : 16, kVals = kBytes / sizeof(T), kRow = kGlrCols / kVals;
+#pragma unroll
+        for (int n = 0; n < kTok * kRow / 32; ++n) {
+            const int id = n * 32 + lane, row = id / kRow, v = (id % kRow) * kVals;
+            const bool ok = row < ntok && c0 + v < C;
+            copy_async<kBytes>(dst + row * kGlrCols + v, src + (ok ? (tok + row) * C + c0 + v : 0), ok ? kBytes : 0);
+        }
+    } else {
+#pragma unroll 8
+        for (int n = 0; n < kWarpVals / 32; ++n) {
+            const int id = n * 32 + lane, row = id / kGlrCols, v = id % kGlrCols;
+            dst[id] = row < ntok && c0 + v < C ? src[(tok + row) * C + c0 + v] : T(0.f);
+        }
+    }
+}
+
+// Tiles by ticket, or strided over the grid where no state is handed on.
+struct Tickets {
+    unsigned int *ticket;
+    int tiles, mine;
+    __device__ __forceinline__ Tickets(unsigned int *t, int n) : ticket(t), tiles(n), mine(blockIdx.x) {}
+    __device__ __forceinline__ int take() {
+        if (ticket) return int(min(atomicAdd(ticket, 1u) + 1u, 0x7fffffffu));  // it starts at all ones
+        const int n = mine;
+        mine = mine > tiles ? mine : mine + int(gridDim.x);
+        return n;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// a block: compute warps, which never wait for one another, and a scan warp
+// ---------------------------------------------------------------------------
+// Each compute warp copies, reads and writes its own eight tokens of every tile,
+// and two tiles are under way: it forms the gates of tile k, leaves their
+// products and sums, and then finishes tile k - 1 from the state that the scan
+// warp has found meanwhile.  The scan warp takes the tickets, joins the warps'
+// sums, publishes them, looks back and hands every warp its starting state.
+template <int NS>
+struct Sync {
+    static constexpr int kInfos = NS + 4;  // tile k + NS + 2 is known while k - 1 is finished
+    uint64_t parts[2], ready[2];
+    Tile tile[kInfos];
+};
+__device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive_cnt(bar, 1);
+}
 
 // ---------------------------------------------------------------------------
 // forward
@@ -287,108 +393,174 @@ struct FwdArgs {
     float *fin, *states;
     GlrPacked pk;
     unsigned int *err;
+    int tiles;
+};
+template <typename T>
+struct FwdPlan {
+    static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
+    static constexpr int kPerSm = 2;
+    struct Stage {
+        T x[kWarpVals], r[kWarpVals], i[kWarpVals];
+    };
+    struct Smem {
+        Stage stage[kStages][kWarps];
+        float4 part[2][kWarps][32];  // products and sums of the warps' tokens
+        float2 start[2][kWarps][32];  // the states before them
+        Sync<kStages> sync;
+    };
+    static constexpr int smem = sizeof(Smem);
 };
 
-template <typename T, bool EVEN, bool PACK>
-__global__ void __launch_bounds__(kWarps * 32)
+template <typename T, bool VEC, bool PACK>
+__global__ void __launch_bounds__(kThreads, FwdPlan<T>::kPerSm)
 glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
-    __shared__ float4 part[kWarps][32];
-    __shared__ float2 hin[32];
-    __shared__ int s_tile;
+    using Plan = FwdPlan<T>;
+    constexpr int NS = Plan::kStages;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    typename Plan::Smem &sm = *reinterpret_cast<typename Plan::Smem *>(smem_raw);
+    Sync<NS> &sync = sm.sync;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (p.ws.ticket) {
-        if (threadIdx.x == 0) s_tile = int(atomicAdd(p.ws.ticket, 1u));
-        __syncthreads();
-    }
-    const Tile t = decode_tile(p.s, p.ws.ticket ? s_tile : int(blockIdx.x), false);
     const int C = p.s.C;
-    const int c = t.ct * kGlrCols + 2 * lane;
-    const bool a0 = c < C, a1 = c + 1 < C;
-    const float A0 = a0 ? __ldg(p.A + c) : 0.f, A1 = a1 ? __ldg(p.A + c + 1) : 0.f;
-
-    float2 xv[kTok], rv[kTok], iv[kTok];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const int tk = warp * kTok + j;
-        const bool ok = tk < t.ntok;
-        const int64_t o = (t.tok + tk) * C + c;
-        xv[j] = load2<T, EVEN>(p.x + o, ok && a0, ok && a1);
-        rv[j] = load2<T, EVEN>(p.r + o, ok && a0, ok && a1);
-        iv[j] = load2<T, EVEN>(p.i + o, ok && a0, ok && a1);
+    Tickets tickets(p.ws.ticket, p.tiles);
+    auto set_tile = [&](int k, int n) {
+        Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        if (n < p.tiles) t = decode_tile(p.s, n, false);
+        else t.tile = -1;
+    };
+    if (threadIdx.x == kWarps * 32) {
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&sync.parts[b], kWarps);
+            tc::mbar_init(&sync.ready[b], 1);
+        }
+        tc::fence_mbar_init();
+        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
     }
-    if (PACK) {
-        const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
+    __syncthreads();
+
+    if (warp == kWarps) {  // the scan warp
+        for (int k = 0;; ++k) {
+            const Tile t = sync.tile[k % Sync<NS>::kInfos];
+            if (t.tile < 0) break;
+            int next = 0;
+            if (lane == 0) next = tickets.take();
+            const int c = t.ct * kGlrCols + 2 * lane;
+            const bool a0 = c < C, a1 = c + 1 < C;
+            float2 h = both(0.f);
+            if (t.first && p.h0) h = load2<VEC>(p.h0 + int64_t(t.row) * C + c, a0, a1);
+            tc::mbar_wait(&sync.parts[k & 1], (k >> 1) & 1, p.err);
+            float4 q[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) q[w] = sm.part[k & 1][w][lane];
+            float2 P = make_float2(q[0].x, q[0].y), S = make_float2(q[0].z, q[0].w);
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float2 d = make_float2(q[w].x, q[w].y);
+                P = mul(P, d);
+                S = fma(d, S, make_float2(q[w].z, q[w].w));
+            }
+            if (!t.first) {
+                if (!t.last) put_sums(p.ws, t.tile, lane, P, S);
+                look_back(p.ws, t, lane, h, p.err);
+            }
+            const float2 out = fma(P, h, S);
+            if (!t.last) put_state(p.ws, t.tile, lane, out);
+            if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, h, a0, a1);
+            if (t.last && p.fin) store2<float, VEC>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                sm.start[k & 1][w][lane] = h;
+                h = fma(make_float2(q[w].x, q[w].y), h, make_float2(q[w].z, q[w].w));
+            }
+            if (lane == 0) set_tile(k + NS + 2, next);
+            arrive_warp(&sync.ready[k & 1], lane);
+        }
+        return;
+    }
+
+    auto load = [&](int k) {
+        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        if (t.tile >= 0) {
+            typename Plan::Stage &st = sm.stage[k % NS][warp];
+            fill<T, VEC>(st.x, p.x, t, C, warp, lane);
+            fill<T, VEC>(st.r, p.r, t, C, warp, lane);
+            fill<T, VEC>(st.i, p.i, t, C, warp, lane);
+        }
+        copy_commit();
+    };
+    struct Held {
+        float2 e1[kTok], u[kTok];
+    };
+    // the gates of tile k; false when there is none
+    auto begin = [&](int k, Held &b) -> bool {
+        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        if (t.tile < 0) return false;
+        const int c = t.ct * kGlrCols + 2 * lane;
+        const bool a0 = c < C, a1 = c + 1 < C;
+        const float2 A = load2<VEC>(p.A + c, a0, a1);
+        const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
+        copy_wait<NS - 1>();
+        __syncwarp();
+        const typename Plan::Stage &st = sm.stage[k % NS][warp];
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
-            const int tk = warp * kTok + j;
-            if (tk >= t.ntok) break;
+            const int o = j * kGlrCols + 2 * lane;
+            const float2 x = unpack2(st.x + o), r = unpack2(st.r + o), i = unpack2(st.i + o);
+            if (PACK && j < ntok) {
+                const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock, row = t.tok + warp * kTok + j;
 #pragma unroll
-            for (int n = 0; n < 3; ++n) {
-                const float2 v = n == 0 ? xv[j] : n == 1 ? rv[j] : iv[j];
-                const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
-                                                                      __float_as_uint(v.y) & 0x7fffffffu));
-                const uint32_t e = pack8_exp(m);
-                const float inv = pack8_inv(e);
-                store_code2<EVEN>(p.pk.codes[n] + (t.tok + tk) * C + c, pack8_code(v.x, inv),
-                                  pack8_code(v.y, inv), a0, a1);
-                if (lane == 0) p.pk.exps[n][(t.tok + tk) * cols8 + t.ct] = uint8_t(e);
+                for (int n = 0; n < 3; ++n) {
+                    const float2 v = n == 0 ? x : n == 1 ? r : i;
+                    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
+                                                                          __float_as_uint(v.y) & 0x7fffffffu));
+                    const uint32_t e = pack8_exp(m);
+                    const float inv = pack8_inv(e);
+                    store_code2<VEC>(p.pk.codes[n] + row * C + c, pack8_code(v.x, inv), pack8_code(v.y, inv), a0, a1);
+                    if (lane == 0) p.pk.exps[n][row * cols8 + t.ct] = uint8_t(e);
+                }
             }
+            const Gate g = gate(r, i, A);
+            b.e1[j] = g.e1;
+            b.u[j] = income(g, x);
         }
-    }
-    float2 e1[kTok], u[kTok];
-    float2 P = make_float2(1.f, 1.f), S = make_float2(0.f, 0.f);
+        if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const bool ok = warp * kTok + j < t.ntok;
-        const Gate g0 = gate(rv[j].x, iv[j].x, A0), g1 = gate(rv[j].y, iv[j].y, A1);
-        // behind the sequence's end: the identity
-        e1[j].x = ok ? g0.e1 : 0.f;
-        e1[j].y = ok ? g1.e1 : 0.f;
-        u[j].x = ok ? g0.v * inv_root(g0.v) * g0.si * xv[j].x : 0.f;
-        u[j].y = ok ? g1.v * inv_root(g1.v) * g1.si * xv[j].y : 0.f;
-        P.x = fmaf(e1[j].x, P.x, P.x);
-        P.y = fmaf(e1[j].y, P.y, P.y);
-        S.x = advance(S.x, e1[j].x, u[j].x);
-        S.y = advance(S.y, e1[j].y, u[j].y);
-    }
-    part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
-    __syncthreads();
-    // the product and sum of the tile's tokens before this warp's
-    float2 Pp = make_float2(1.f, 1.f), Sp = make_float2(0.f, 0.f);
-    for (int v = 0; v < warp; ++v) {
-        const float4 q = part[v][lane];
-        Pp.x *= q.x;
-        Pp.y *= q.y;
-        Sp.x = fmaf(q.x, Sp.x, q.z);
-        Sp.y = fmaf(q.y, Sp.y, q.w);
-    }
-    if (warp == kWarps - 1) {
-        const float2 Pt = make_float2(Pp.x * P.x, Pp.y * P.y);
-        const float2 St = make_float2(fmaf(P.x, Sp.x, S.x), fmaf(P.y, Sp.y, S.y));
-        float2 h = make_float2(0.f, 0.f);
-        if (t.first) {
-            if (p.h0) h = load2<float, EVEN>(p.h0 + int64_t(t.row) * C + c, a0, a1);
-        } else {
-            if (!t.last) publish_sums(p.ws, t, Pt, St, lane);
-            look_back(p.ws, t, lane, h, p.err);
+            for (int j = 0; j < kTok; ++j)
+                if (j >= ntok) b.e1[j] = b.u[j] = both(0.f);
         }
-        const float2 out = make_float2(fmaf(Pt.x, h.x, St.x), fmaf(Pt.y, h.y, St.y));
-        if (!t.last) publish_state(p.ws, t, out, lane);
-        hin[lane] = h;
-        if (p.states) store2<float, EVEN>(p.states + t.chunk * C + c, h, a0, a1);
-        if (t.last && p.fin) store2<float, EVEN>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
-    }
-    __syncthreads();
-    float2 h = hin[lane];
-    h.x = fmaf(Pp.x, h.x, Sp.x);
-    h.y = fmaf(Pp.y, h.y, Sp.y);
+        float2 P = both(1.f), S = both(0.f);
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const int tk = warp * kTok + j;
-        if (tk >= t.ntok) break;
-        h.x = advance(h.x, e1[j].x, u[j].x);
-        h.y = advance(h.y, e1[j].y, u[j].y);
-        store2<T, EVEN>(p.y + (t.tok + tk) * C + c, h, a0, a1);
+        for (int j = 0; j < kTok; ++j) {
+            P = fma(b.e1[j], P, P);
+            S = advance(S, b.e1[j], b.u[j]);
+        }
+        sm.part[k & 1][warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+        arrive_warp(&sync.parts[k & 1], lane);  // and this warp's part of the stage is read
+        load(k + NS);
+        return true;
+    };
+    auto finish = [&](int k, const Held &b) {
+        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const int c = t.ct * kGlrCols + 2 * lane;
+        const bool a0 = c < C, a1 = c + 1 < C;
+        const int ntok = t.ntok - warp * kTok;
+        T *y = p.y + (t.tok + warp * kTok) * C + c;
+        tc::mbar_wait(&sync.ready[k & 1], (k >> 1) & 1, p.err);
+        float2 h = sm.start[k & 1][warp][lane];
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            h = advance(h, b.e1[j], b.u[j]);
+            if (j < ntok) store2<T, VEC>(y + int64_t(j) * C, h, a0, a1);
+        }
+    };
+    for (int k = 0; k < NS; ++k) load(k);
+    Held a, b;
+    for (int k = 0;; k += 2) {
+        const bool more = begin(k, a);
+        if (k > 0) finish(k - 1, b);
+        if (!more) break;
+        const bool again = begin(k + 1, b);
+        finish(k, a);
+        if (!again) break;
     }
 }
 
@@ -405,153 +577,247 @@ struct BwdArgs {
     T *dx, *dr, *di;
     float *dinit, *dA_part;
     unsigned int *err;
+    int tiles;
+};
+template <typename T, bool PACK>
+struct BwdPlan {
+    static constexpr int kStages = 3;  // two tiles under way, one on the way
+    static constexpr int kPerSm = sizeof(T) == 2 ? 2 : 1;
+    using In = std::conditional_t<PACK, int8_t, T>;
+    struct Stage {
+        In in[3][kWarpVals];
+        T dy[kWarpVals];
+        uint32_t exps[PACK ? 3 : 1][kTok];  // the words that hold the exponent bytes
+    };
+    struct Smem {
+        Stage stage[kStages][kWarps];
+        float4 part[2][kWarps][32];   // products, forward sums
+        float2 rpart[2][kWarps][32];  // reverse sums
+        float2 dA[2][kWarps][32];
+        float4 start[2][kWarps][32];  // the state before the warp's tokens, K behind them
+        Sync<kStages> sync;
+    };
+    static constexpr int smem = sizeof(Smem);
 };
 
-template <typename T, bool EVEN, bool PACK>
-__global__ void __launch_bounds__(kWarps * 32)
+template <typename T, bool VEC, bool PACK>
+__global__ void __launch_bounds__(kThreads, BwdPlan<T, PACK>::kPerSm)
 glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
-    __shared__ float4 part[kWarps][32];   // products, forward sums
-    __shared__ float2 rpart[kWarps][32];  // reverse sums, then dA
-    __shared__ float2 kin[32];
-    __shared__ int s_tile;
+    using Plan = BwdPlan<T, PACK>;
+    constexpr int NS = Plan::kStages;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    typename Plan::Smem &sm = *reinterpret_cast<typename Plan::Smem *>(smem_raw);
+    Sync<NS> &sync = sm.sync;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (p.ws.ticket) {
-        if (threadIdx.x == 0) s_tile = int(atomicAdd(p.ws.ticket, 1u));
-        __syncthreads();
-    }
-    const Tile t = decode_tile(p.s, p.ws.ticket ? s_tile : int(blockIdx.x), true);
     const int C = p.s.C;
-    const int c = t.ct * kGlrCols + 2 * lane;
-    const bool a0 = c < C, a1 = c + 1 < C;
-    const float A0 = a0 ? __ldg(p.A + c) : 0.f, A1 = a1 ? __ldg(p.A + c + 1) : 0.f;
-    const float2 h0 = load2<float, EVEN>(p.states + t.chunk * C + c, a0, a1);
-
-    float2 xv[kTok], rv[kTok], iv[kTok], dv[kTok];
     const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
+    Tickets tickets(p.ws.ticket, p.tiles);
+    auto set_tile = [&](int k, int n) {
+        Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        if (n < p.tiles) t = decode_tile(p.s, n, true);
+        else t.tile = -1;
+    };
+    if (threadIdx.x == kWarps * 32) {
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&sync.parts[b], kWarps);
+            tc::mbar_init(&sync.ready[b], 1);
+        }
+        tc::fence_mbar_init();
+        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
+    }
+    __syncthreads();
+
+    if (warp == kWarps) {  // the scan warp
+        // dA of tile k, which its warps have left by the time they leave the sums of tile k + 2
+        auto sum_dA = [&](int k) {
+            const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+            const int c = t.ct * kGlrCols + 2 * lane;
+            float2 sum = sm.dA[k & 1][0][lane];
 #pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const int tk = warp * kTok + j;
-        const bool ok = tk < t.ntok;
-        const int64_t o = (t.tok + tk) * C + c;
-        dv[j] = load2<T, EVEN>(p.dy + o, ok && a0, ok && a1);
-        if (PACK) {
-            const int64_t b = (t.tok + tk) * cols8 + t.ct;
-            xv[j] = load_code2<EVEN>(p.pk.codes[0] + o, ok ? pack8_step(__ldg(p.pk.exps[0] + b)) : 0.f, ok && a0, ok && a1);
-            rv[j] = load_code2<EVEN>(p.pk.codes[1] + o, ok ? pack8_step(__ldg(p.pk.exps[1] + b)) : 0.f, ok && a0, ok && a1);
-            iv[j] = load_code2<EVEN>(p.pk.codes[2] + o, ok ? pack8_step(__ldg(p.pk.exps[2] + b)) : 0.f, ok && a0, ok && a1);
+            for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[k & 1][w][lane]);
+            store2<float, VEC>(p.dA_part + t.chunk * C + c, sum, c < C, c + 1 < C);
+        };
+        int k = 0;
+        for (;; ++k) {
+            const Tile t = sync.tile[k % Sync<NS>::kInfos];
+            if (t.tile < 0) break;
+            int next = 0;
+            if (lane == 0) next = tickets.take();
+            const int c = t.ct * kGlrCols + 2 * lane;
+            const bool a0 = c < C, a1 = c + 1 < C;
+            float2 h = load2<VEC>(p.states + t.chunk * C + c, a0, a1), K = both(0.f);
+            if (t.last && p.dfin) K = load2<VEC>(p.dfin + int64_t(t.row) * C + c, a0, a1);
+            tc::mbar_wait(&sync.parts[k & 1], (k >> 1) & 1, p.err);
+            float2 q[kWarps], z[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 v = sm.part[k & 1][w][lane];
+                q[w] = make_float2(v.x, v.y);
+                z[w] = sm.rpart[k & 1][w][lane];
+                *reinterpret_cast<float2 *>(&sm.start[k & 1][w][lane]) = h;
+                h = fma(q[w], h, make_float2(v.z, v.w));
+            }
+            float2 P = q[kWarps - 1], R = z[kWarps - 1];
+#pragma unroll
+            for (int w = kWarps - 2; w >= 0; --w) {
+                P = mul(P, q[w]);
+                R = fma(q[w], R, z[w]);
+            }
+            if (!t.last) {
+                if (!t.first) put_sums(p.ws, t.tile, lane, P, R);
+                look_back(p.ws, t, lane, K, p.err);
+            }
+            const float2 out = fma(P, K, R);
+            if (!t.first) put_state(p.ws, t.tile, lane, out);
+            if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) {
+                reinterpret_cast<float2 *>(&sm.start[k & 1][w][lane])[1] = K;
+                K = fma(q[w], K, z[w]);
+            }
+            if (k >= 2) sum_dA(k - 2);
+            __syncwarp();
+            if (lane == 0) set_tile(k + NS + 2, next);
+            arrive_warp(&sync.ready[k & 1], lane);
+        }
+        // the last two tiles: their warps say when they are through
+        for (int j = k < 2 ? 0 : k - 2; j < k; ++j) {
+            tc::mbar_wait(&sync.parts[(j + 2) & 1], ((j + 2) >> 1) & 1, p.err);
+            sum_dA(j);
+        }
+        return;
+    }
+
+    auto load = [&](int k) {
+        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        if (t.tile >= 0) {
+            typename Plan::Stage &st = sm.stage[k % NS][warp];
+            if constexpr (PACK) {
+#pragma unroll
+                for (int n = 0; n < 3; ++n) fill<int8_t, VEC>(st.in[n], p.pk.codes[n], t, C, warp, lane);
+                // the aligned word around each exponent byte, as far as the array goes
+                if (lane < 3 * kTok) {
+                    const int n = lane / kTok, row = warp * kTok + lane % kTok;
+                    const uint8_t *e = n == 0 ? p.pk.exps[0] : n == 1 ? p.pk.exps[1] : p.pk.exps[2];
+                    const int64_t all = int64_t(p.s.batch) * p.s.T * cols8;
+                    const int64_t at = row < t.ntok ? ((t.tok + row) * cols8 + t.ct) & ~int64_t(3) : 0;
+                    copy_async<4>(&st.exps[n][lane % kTok], e + at, int(all - at < 4 ? all - at : 4));
+                }
+            } else {
+                fill<T, VEC>(st.in[0], p.x, t, C, warp, lane);
+                fill<T, VEC>(st.in[1], p.r, t, C, warp, lane);
+                fill<T, VEC>(st.in[2], p.i, t, C, warp, lane);
+            }
+            fill<T, VEC>(st.dy, p.dy, t, C, warp, lane);
+        }
+        copy_commit();
+    };
+    struct Held {
+        float2 e1[kTok], u[kTok];
+    };
+    // x, r or i of token j of this warp
+    auto input = [&](const typename Plan::Stage &st, const Tile &t, int n, int j) -> float2 {
+        const int o = j * kGlrCols + 2 * lane;
+        if constexpr (PACK) {
+            const uint32_t shift = 8 * uint32_t(((t.tok + warp * kTok + j) * cols8 + t.ct) & 3);
+            const float step = pack8_step((st.exps[n][j] >> shift) & 255u);
+            const char2 q = *reinterpret_cast<const char2 *>(st.in[n] + o);
+            return make_float2(float(q.x) * step, float(q.y) * step);
         } else {
-            xv[j] = load2<T, EVEN>(p.x + o, ok && a0, ok && a1);
-            rv[j] = load2<T, EVEN>(p.r + o, ok && a0, ok && a1);
-            iv[j] = load2<T, EVEN>(p.i + o, ok && a0, ok && a1);
+            return unpack2(st.in[n] + o);
+        }
+    };
+    auto begin = [&](int k, Held &b) -> bool {
+        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        if (t.tile < 0) return false;
+        const int c = t.ct * kGlrCols + 2 * lane;
+        const float2 A = load2<VEC>(p.A + c, c < C, c + 1 < C);
+        const int ntok = t.ntok - warp * kTok;
+        copy_wait<NS - 2>();
+        __syncwarp();
+        const typename Plan::Stage &st = sm.stage[k % NS][warp];
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            const Gate g = gate(input(st, t, 1, j), input(st, t, 2, j), A);
+            b.e1[j] = g.e1;
+            b.u[j] = income(g, input(st, t, 0, j));
+        }
+        if (ntok < kTok) {
+#pragma unroll
+            for (int j = 0; j < kTok; ++j)
+                if (j >= ntok) b.e1[j] = b.u[j] = both(0.f);
+        }
+        float2 P = both(1.f), S = both(0.f), R = both(0.f);
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            P = fma(b.e1[j], P, P);
+            S = advance(S, b.e1[j], b.u[j]);
+        }
+#pragma unroll
+        for (int j = kTok - 1; j >= 0; --j) {
+            R = add(R, unpack2(st.dy + j * kGlrCols + 2 * lane));  // 0 behind the end
+            R = fma(b.e1[j], R, R);
+        }
+        sm.part[k & 1][warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+        sm.rpart[k & 1][warp][lane] = R;
+        arrive_warp(&sync.parts[k & 1], lane);
+        return true;
+    };
+    auto finish = [&](int k, Held &b) {
+        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const int c = t.ct * kGlrCols + 2 * lane;
+        const bool a0 = c < C, a1 = c + 1 < C;
+        const float2 A = load2<VEC>(p.A + c, a0, a1);
+        const int ntok = t.ntok - warp * kTok;
+        const int64_t base = (t.tok + warp * kTok) * C + c;
+        const typename Plan::Stage &st = sm.stage[k % NS][warp];
+        tc::mbar_wait(&sync.ready[k & 1], (k >> 1) & 1, p.err);
+        const float4 s = sm.start[k & 1][warp][lane];
+        float2 h = make_float2(s.x, s.y), K = make_float2(s.z, s.w), dA = both(0.f);
+        // u[j] becomes the state before the token
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            const float2 before = h;
+            h = advance(h, b.e1[j], b.u[j]);
+            b.u[j] = before;
+        }
+#pragma unroll
+        for (int j = kTok - 1; j >= 0; --j) {
+            if (j >= ntok) continue;
+            const float2 x = input(st, t, 0, j);
+            const Gate g = gate(input(st, t, 1, j), input(st, t, 2, j), A);
+            const float2 rs = make_float2(inv_root(g.w.x), inv_root(g.w.y));
+            const float2 a = add(g.e1, both(1.f)), six = mul(g.si, x);
+            const float2 G = add(K, unpack2(st.dy + j * kGlrCols + 2 * lane));
+            const float2 Gm = mul(mul(G, rs), make_float2(-g.w.x, -g.w.y));
+            const float2 as = mul(mul(a, six), rs);
+            const float2 dl = mul(mul(G, a), add(b.u[j], make_float2(-as.x, -as.y)));
+            dA = fma(dl, g.sr, dA);
+            K = fma(g.e1, G, G);
+            store2<T, VEC>(p.dx + base + int64_t(j) * C, mul(Gm, g.si), a0, a1);
+            store2<T, VEC>(p.di + base + int64_t(j) * C, mul(mul(Gm, six), mul(g.ei, g.si)), a0, a1);
+            store2<T, VEC>(p.dr + base + int64_t(j) * C, mul(mul(dl, g.l), mul(g.er, g.sr)), a0, a1);
+        }
+        sm.dA[k & 1][warp][lane] = dA;
+        __syncwarp();  // this warp's part of the stage is read
+        load(k + NS);
+    };
+    for (int k = 0; k < NS; ++k) load(k);
+    Held a, b;
+    int k = 0;
+    for (;; k += 2) {
+        const bool more = begin(k, a);
+        if (k > 0) finish(k - 1, b);
+        if (!more) break;
+        const bool again = begin(k + 1, b);
+        finish(k, a);
+        if (!again) {
+            ++k;
+            break;
         }
     }
-    float2 e1[kTok], u[kTok];
-    float2 P = make_float2(1.f, 1.f), S = make_float2(0.f, 0.f), R = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const bool ok = warp * kTok + j < t.ntok;
-        const Gate g0 = gate(rv[j].x, iv[j].x, A0), g1 = gate(rv[j].y, iv[j].y, A1);
-        e1[j].x = ok ? g0.e1 : 0.f;
-        e1[j].y = ok ? g1.e1 : 0.f;
-        u[j].x = ok ? g0.v * inv_root(g0.v) * g0.si * xv[j].x : 0.f;
-        u[j].y = ok ? g1.v * inv_root(g1.v) * g1.si * xv[j].y : 0.f;
-        P.x = fmaf(e1[j].x, P.x, P.x);
-        P.y = fmaf(e1[j].y, P.y, P.y);
-        S.x = advance(S.x, e1[j].x, u[j].x);
-        S.y = advance(S.y, e1[j].y, u[j].y);
-    }
-#pragma unroll
-    for (int j = kTok - 1; j >= 0; --j) {
-        R.x += dv[j].x;
-        R.y += dv[j].y;
-        R.x = fmaf(e1[j].x, R.x, R.x);
-        R.y = fmaf(e1[j].y, R.y, R.y);
-    }
-    part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
-    rpart[warp][lane] = R;
-    __syncthreads();
-    // the state before this warp's tokens, and the reverse sums behind them
-    float2 h = h0;
-    for (int v = 0; v < warp; ++v) {
-        const float4 q = part[v][lane];
-        h.x = fmaf(q.x, h.x, q.z);
-        h.y = fmaf(q.y, h.y, q.w);
-    }
-    float2 Pp = make_float2(1.f, 1.f), Rp = make_float2(0.f, 0.f);
-    for (int v = kWarps - 1; v > warp; --v) {
-        const float4 q = part[v][lane];
-        const float2 z = rpart[v][lane];
-        Pp.x *= q.x;
-        Pp.y *= q.y;
-        Rp.x = fmaf(q.x, Rp.x, z.x);
-        Rp.y = fmaf(q.y, Rp.y, z.y);
-    }
-    if (warp == 0) {
-        const float2 Pt = make_float2(Pp.x * P.x, Pp.y * P.y);
-        const float2 Rt = make_float2(fmaf(P.x, Rp.x, R.x), fmaf(P.y, Rp.y, R.y));
-        float2 K = make_float2(0.f, 0.f);
-        if (t.last) {
-            if (p.dfin) K = load2<float, EVEN>(p.dfin + int64_t(t.row) * C + c, a0, a1);
-        } else {
-            if (!t.first) publish_sums(p.ws, t, Pt, Rt, lane);
-            look_back(p.ws, t, lane, K, p.err);
-        }
-        const float2 out = make_float2(fmaf(Pt.x, K.x, Rt.x), fmaf(Pt.y, K.y, Rt.y));
-        if (!t.first) publish_state(p.ws, t, out, lane);
-        kin[lane] = K;
-        if (t.first && p.dinit) store2<float, EVEN>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
-    }
-    __syncthreads();
-    float2 K = kin[lane];
-    K.x = fmaf(Pp.x, K.x, Rp.x);
-    K.y = fmaf(Pp.y, K.y, Rp.y);
-    // u[j] becomes the state before the token
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-        const float2 before = h;
-        h.x = advance(h.x, e1[j].x, u[j].x);
-        h.y = advance(h.y, e1[j].y, u[j].y);
-        u[j] = before;
-    }
-    float2 dA = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = kTok - 1; j >= 0; --j) {
-        const int tk = warp * kTok + j;
-        const bool ok = tk < t.ntok;
-        float dxv[2], drv[2], div[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float A = q ? A1 : A0, xq = q ? xv[j].y : xv[j].x, hq = q ? u[j].y : u[j].x;
-            float &Kq = q ? K.y : K.x;
-            const Gate g = gate(q ? rv[j].y : rv[j].x, q ? iv[j].y : iv[j].x, A);
-            const float rs = inv_root(g.v), m = g.v * rs, a = 1.f + g.e1;
-            const float G = (q ? dv[j].y : dv[j].x) + Kq;
-            const float six = g.si * xq;
-            const float dl = G * a * (hq - a * six * rs);
-            dxv[q] = G * m * g.si;
-            div[q] = G * m * six * g.ci;
-            drv[q] = dl * g.l * g.cr;
-            (q ? dA.y : dA.x) += ok ? dl * g.sr : 0.f;
-            Kq = ok ? fmaf(g.e1, G, G) : Kq;
-        }
-        if (!ok) continue;
-        const int64_t o = (t.tok + tk) * C + c;
-        store2<T, EVEN>(p.dx + o, make_float2(dxv[0], dxv[1]), a0, a1);
-        store2<T, EVEN>(p.dr + o, make_float2(drv[0], drv[1]), a0, a1);
-        store2<T, EVEN>(p.di + o, make_float2(div[0], div[1]), a0, a1);
-    }
-    __syncthreads();  // rpart is read above
-    rpart[warp][lane] = dA;
-    __syncthreads();
-    if (warp == 0) {
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int v = 0; v < kWarps; ++v) {
-            sum.x += rpart[v][lane].x;
-            sum.y += rpart[v][lane].y;
-        }
-        store2<float, EVEN>(p.dA_part + t.chunk * C + c, sum, a0, a1);
-    }
+    // k tiles are through; the scan warp sums the last two's dA behind two more arrivals
+    for (int j = 0; j < 2; ++j) arrive_warp(&sync.parts[(k + j) & 1], lane);
 }
 
 // Column sums of a [rows, C] array: 32 columns a block, 32 rows at a time, each
@@ -575,32 +841,46 @@ row_sum_kernel(const float *__restrict__ part, int64_t rows, int C, float *__res
 // ---------------------------------------------------------------------------
 // decode step
 // ---------------------------------------------------------------------------
-template <typename T, bool EVEN>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
 glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                 const float *__restrict__ A, float *__restrict__ state, T *__restrict__ y) {
     const int c = (blockIdx.x * 256 + threadIdx.x) * 2;
     const bool a0 = c < C, a1 = c + 1 < C;
     if (!a0) return;
-    const float A0 = __ldg(A + c), A1 = a1 ? __ldg(A + c + 1) : 0.f;
+    const float2 Av = load2<VEC>(A + c, a0, a1);
     for (int b = blockIdx.y; b < batch; b += gridDim.y) {
         const int64_t o = int64_t(b) * C + c;
-        const float2 xv = load2<T, EVEN>(x + o, a0, a1), rv = load2<T, EVEN>(r + o, a0, a1),
-                     iv = load2<T, EVEN>(i + o, a0, a1);
-        float2 h;
-        if (EVEN) h = *reinterpret_cast<const float2 *>(state + o);
-        else h = make_float2(state[o], a1 ? state[o + 1] : 0.f);
-        const Gate g0 = gate(rv.x, iv.x, A0), g1 = gate(rv.y, iv.y, A1);
-        h.x = advance(h.x, g0.e1, g0.v * inv_root(g0.v) * g0.si * xv.x);
-        h.y = advance(h.y, g1.e1, g1.v * inv_root(g1.v) * g1.si * xv.y);
-        store2<float, EVEN>(state + o, h, a0, a1);
-        store2<T, EVEN>(y + o, h, a0, a1);
+        float2 xv, rv, iv, h;
+        if (VEC) {
+            xv = unpack2(x + o); rv = unpack2(r + o); iv = unpack2(i + o);
+            h = *reinterpret_cast<const float2 *>(state + o);
+        } else {
+            const int64_t n = a1 ? o + 1 : o;
+            xv = make_float2(to_f32<T>(x[o]), to_f32<T>(x[n]));
+            rv = make_float2(to_f32<T>(r[o]), to_f32<T>(r[n]));
+            iv = make_float2(to_f32<T>(i[o]), to_f32<T>(i[n]));
+            h = make_float2(state[o], state[n]);
+        }
+        const Gate g = gate(rv, iv, Av);
+        h = advance(h, g.e1, income(g, xv));
+        store2<float, VEC>(state + o, h, a0, a1);
+        store2<T, VEC>(y + o, h, a0, a1);
     }
 }
 
-int64_t tiles_of(const GlrShape &s) { return int64_t(s.nct) * s.nc * (s.nseq ? 1 : s.batch); }
+// A persistent grid: as many blocks as the GPU holds at once, or one a tile.
+template <typename K, typename A>
+cudaError_t launch_tiles(K kernel, int smem, int per_sm, const GlrShape &s, A &a, cudaStream_t stream) {
+    const int64_t tiles = int64_t(s.nct) * s.nc * (s.nseq ? 1 : s.batch);
+    const int64_t room = int64_t(device_sm_count()) * per_sm;
+    a.tiles = int(tiles);
+    if (!smem_attr_once(reinterpret_cast<const void *>(kernel), smem)) return cudaErrorInvalidValue;
+    kernel<<<unsigned(tiles < room ? tiles : room), kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
 
-template <typename T, bool EVEN, bool PACK>
+template <typename T, bool VEC, bool PACK>
 cudaError_t forward_typed(const GlrShape &s, const void *x, const void *r, const void *i, const float *A,
                           const float *h0, void *y, float *fin, float *states, const GlrPacked *packed,
                           const GlrScratch &ws, unsigned int *err, cudaStream_t stream) {
@@ -610,11 +890,10 @@ cudaError_t forward_typed(const GlrShape &s, const void *x, const void *r, const
     a.A = A; a.h0 = h0; a.y = static_cast<T *>(y); a.fin = fin; a.states = states;
     a.pk = packed ? *packed : GlrPacked{};
     a.err = err;
-    glr_forward_kernel<T, EVEN, PACK><<<unsigned(tiles_of(s)), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_tiles(glr_forward_kernel<T, VEC, PACK>, FwdPlan<T>::smem, FwdPlan<T>::kPerSm, s, a, stream);
 }
 
-template <typename T, bool EVEN, bool PACK>
+template <typename T, bool VEC, bool PACK>
 cudaError_t backward_typed(const GlrShape &s, const void *x, const void *r, const void *i, const GlrPacked *packed,
                            const float *A, const float *states, const void *dy, const float *dfin, void *dx,
                            void *dr, void *di, float *dinit, float *dA_part, const GlrScratch &ws,
@@ -627,9 +906,11 @@ cudaError_t backward_typed(const GlrShape &s, const void *x, const void *r, cons
     a.A = A; a.states = states; a.dfin = dfin;
     a.dx = static_cast<T *>(dx); a.dr = static_cast<T *>(dr); a.di = static_cast<T *>(di);
     a.dinit = dinit; a.dA_part = dA_part; a.err = err;
-    glr_backward_kernel<T, EVEN, PACK><<<unsigned(tiles_of(s)), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_tiles(glr_backward_kernel<T, VEC, PACK>, BwdPlan<T, PACK>::smem, BwdPlan<T, PACK>::kPerSm, s, a, stream);
 }
+
+// rows of whole 16-byte vectors
+bool vectors(int C, bool bf16) { return C % (bf16 ? 8 : 4) == 0; }
 
 // Calls f with the storage type and two truth values as types.
 template <typename F>
@@ -648,7 +929,7 @@ cudaError_t launch_glr_forward(const GlrShape &s, bool bf16, const void *x, cons
                                const float *A, const float *h0, void *y, float *fin, float *states,
                                const GlrPacked *packed, const GlrScratch &ws, unsigned int *err,
                                cudaStream_t stream) {
-    return by_type(bf16, s.C % 2 == 0, packed != nullptr, [&](auto t, auto even, auto pack) {
+    return by_type(bf16, vectors(s.C, bf16), packed != nullptr, [&](auto t, auto even, auto pack) {
         return forward_typed<decltype(t), decltype(even)::value, decltype(pack)::value>(
             s, x, r, i, A, h0, y, fin, states, packed, ws, err, stream);
     });
@@ -658,7 +939,7 @@ cudaError_t launch_glr_backward(const GlrShape &s, bool bf16, const void *x, con
                                 const GlrPacked *packed, const float *A, const float *states, const void *dy,
                                 const float *dfin, void *dx, void *dr, void *di, float *dinit, float *dA_part,
                                 const GlrScratch &ws, unsigned int *err, cudaStream_t stream) {
-    return by_type(bf16, s.C % 2 == 0, packed != nullptr, [&](auto t, auto even, auto pack) {
+    return by_type(bf16, s.C % 8 == 0, packed != nullptr, [&](auto t, auto even, auto pack) {
         return backward_typed<decltype(t), decltype(even)::value, decltype(pack)::value>(
             s, x, r, i, packed, A, states, dy, dfin, dx, dr, di, dinit, dA_part, ws, err, stream);
     });
