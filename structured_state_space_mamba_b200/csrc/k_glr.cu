@@ -64,52 +64,60 @@ __device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a,
 __device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-struct Gate {
+// Operations with a constant stay scalar: there it is an immediate, while a packed
+// operation needs it in a pair of registers (moving those there cost a quarter
+// of all instructions).
+__device__ __forceinline__ float2 scale(float2 a, float c) { return make_float2(a.x * c, a.y * c); }
+__device__ __forceinline__ float2 plus(float2 a, float c) { return make_float2(a.x + c, a.y + c); }
+__device__ __forceinline__ float2 times_plus(float2 a, float2 b, float c) {
+    return make_float2(fmaf(a.x, b.x, c), fmaf(a.y, b.y, c));
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The two sigmoids.  One reciprocal serves both; the arguments are held at -43 so
+// that the product of the denominators stays finite (s(-43) = 2e-19).
+struct Sig {
     float2 sr, si;  // s(r), s(i)
     float2 er, ei;  // e^-r, e^-i: 1 - s(r) = er * sr
-    float2 l, e1;   // log decay, decay - 1
-    float2 w;       // decay^2 - 1
 };
-
-// e^l - 1 for l <= 0: the Taylor sum to l^7 from -1/2 up (the next term is below
-// 2^-22 of the result there), the exponential below (where its error is no
-// longer magnified by the difference).
-__device__ __forceinline__ float2 decay_minus_1(float2 l) {
-    float2 p = fma(l, both(1.f / 5040.f), both(1.f / 720.f));
-    p = fma(l, p, both(1.f / 120.f));
-    p = fma(l, p, both(1.f / 24.f));
-    p = fma(l, p, both(1.f / 6.f));
-    p = fma(l, p, both(0.5f));
-    p = fma(l, p, both(1.f));
-    p = mul(p, l);
-    if (fminf(l.x, l.y) < -0.5f) {
-        if (l.x < -0.5f) p.x = ex2(l.x * 1.4426950408889634f) - 1.f;
-        if (l.y < -0.5f) p.y = ex2(l.y * 1.4426950408889634f) - 1.f;
-    }
-    return p;
-}
-
-// One reciprocal serves both sigmoids; the arguments are held at -43 so that
-// the product of the two denominators stays finite (s(-43) = 2e-19).
-__device__ __forceinline__ Gate gate(float2 r, float2 i, float2 A) {
-    Gate g;
-    const float2 k = both(-1.4426950408889634f);
-    const float2 tr = mul(make_float2(max_nan(r.x, -43.f), max_nan(r.y, -43.f)), k);
-    const float2 ti = mul(make_float2(max_nan(i.x, -43.f), max_nan(i.y, -43.f)), k);
-    g.er = make_float2(ex2(tr.x), ex2(tr.y));
-    g.ei = make_float2(ex2(ti.x), ex2(ti.y));
-    const float2 dr = add(g.er, both(1.f)), di = add(g.ei, both(1.f));
+__device__ __forceinline__ Sig sigmoids(float2 r, float2 i) {
+    Sig g;
+    g.er = make_float2(ex2(max_nan(r.x, -43.f) * -kLog2e), ex2(max_nan(r.y, -43.f) * -kLog2e));
+    g.ei = make_float2(ex2(max_nan(i.x, -43.f) * -kLog2e), ex2(max_nan(i.y, -43.f) * -kLog2e));
+    const float2 dr = plus(g.er, 1.f), di = plus(g.ei, 1.f);
     const float2 d = mul(dr, di), q = make_float2(rcp(d.x), rcp(d.y));
     g.sr = mul(di, q);
     g.si = mul(dr, q);
-    g.l = mul(A, g.sr);
-    g.e1 = decay_minus_1(g.l);
-    g.w = mul(g.e1, add(g.e1, both(2.f)));
     return g;
 }
-// what a token brings in: sqrt(1 - a^2) s(i) x
-__device__ __forceinline__ float2 income(const Gate &g, float2 x) {
-    return mul(mul(make_float2(root(-g.w.x), root(-g.w.y)), g.si), x);
+// Whether some decay of the warp's channels can fall below e^-1/2 (|l| <= |A|).
+__device__ __forceinline__ bool steep_warp(float2 A) {
+    return __any_sync(0xffffffffu, A.x < -0.5f || A.y < -0.5f);
+}
+// e^l - 1 for l <= 0: the Taylor sum to l^7 from -1/2 up (the next term is below
+// 2^-22 of the result there), the exponential below (where its error is no
+// longer magnified by the difference).
+__device__ __forceinline__ float2 decay_minus_1(float2 l, bool steep) {
+    float2 p = make_float2(fmaf(l.x, 1.f / 5040.f, 1.f / 720.f), fmaf(l.y, 1.f / 5040.f, 1.f / 720.f));
+    p = times_plus(l, p, 1.f / 120.f);
+    p = times_plus(l, p, 1.f / 24.f);
+    p = times_plus(l, p, 1.f / 6.f);
+    p = times_plus(l, p, 0.5f);
+    p = fma(mul(l, p), l, l);
+    if (steep) {
+        const float2 e = make_float2(ex2(l.x * kLog2e) - 1.f, ex2(l.y * kLog2e) - 1.f);
+        p = make_float2(l.x < -0.5f ? e.x : p.x, l.y < -0.5f ? e.y : p.y);
+    }
+    return p;
+}
+// a^2 - 1 from a - 1
+__device__ __forceinline__ float2 square_minus_1(float2 e1) { return fma(e1, e1, add(e1, e1)); }
+// decay - 1 and what the token brings in, sqrt(1 - a^2) s(i) x
+__device__ __forceinline__ void token(float2 x, float2 r, float2 i, float2 A, bool steep, float2 &e1, float2 &u) {
+    const Sig g = sigmoids(r, i);
+    e1 = decay_minus_1(mul(A, g.sr), steep);
+    const float2 w = square_minus_1(e1);
+    u = mul(make_float2(root(-w.x), root(-w.y)), mul(g.si, x));
 }
 // 1 / sqrt(-w), 0 for 0
 __device__ __forceinline__ float inv_root(float w) { return w == 0.f ? 0.f : rsq(-w); }
@@ -326,25 +334,34 @@ constexpr int kThreads = 32 * (kWarps + 1);   // and the scan warp
 constexpr int kTok = kGlrChunk / kWarps;      // tokens of a warp
 constexpr int kWarpVals = kTok * kGlrCols;
 
-// One warp's tokens of a tile of a [tokens, C] array; zeros where there is nothing.
-template <typename T, bool VEC>
-__device__ __forceinline__ void fill(T *dst, const T *src, const Tile &t, int C, int warp, int lane) {
+// Copies one warp's tokens of a tile of N [tokens, C] arrays; zeros where there is
+// nothing.  The places are the same in all of them and are worked out once.
+template <typename T, bool VEC, int N>
+__device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N], const Tile &t, int C, int warp,
+                                     int lane) {
     const int c0 = t.ct * kGlrCols, ntok = t.ntok - warp * kTok;
     const int64_t tok = t.tok + warp * kTok;
     if (VEC) {
         constexpr int kBytes = sizeof(T) == 1 ? 8 : 16, kVals = kBytes / sizeof(T), kRow = kGlrCols / kVals;
+        constexpr int kRows = 32 / kRow;  // tokens of one step
+        const int row = lane / kRow, v = (lane % kRow) * kVals;
+        const bool in = c0 + v < C;
+        int64_t o = (tok + row) * C + c0 + v;
 #pragma unroll
-        for (int n = 0; n < kTok * kRow / 32; ++n) {
-            const int id = n * 32 + lane, row = id / kRow, v = (id % kRow) * kVals;
-            const bool ok = row < ntok && c0 + v < C;
-            copy_async<kBytes>(dst + row * kGlrCols + v, src + (ok ? (tok + row) * C + c0 + v : 0), ok ? kBytes : 0);
+        for (int n = 0; n < kTok / kRows; ++n, o += int64_t(kRows) * C) {
+            const bool ok = in && row + n * kRows < ntok;
+#pragma unroll
+            for (int a = 0; a < N; ++a)
+                copy_async<kBytes>(dst[a] + n * kRows * kGlrCols + lane * kVals, src[a] + (ok ? o : 0), ok ? kBytes : 0);
         }
     } else {
+#pragma unroll
+        for (int a = 0; a < N; ++a)
 #pragma unroll 8
-        for (int n = 0; n < kWarpVals / 32; ++n) {
-            const int id = n * 32 + lane, row = id / kGlrCols, v = id % kGlrCols;
-            dst[id] = row < ntok && c0 + v < C ? src[(tok + row) * C + c0 + v] : T(0.f);
-        }
+            for (int n = 0; n < kWarpVals / 32; ++n) {
+                const int id = n * 32 + lane, row = id / kGlrCols, v = id % kGlrCols;
+                dst[a][id] = row < ntok && c0 + v < C ? src[a][(tok + row) * C + c0 + v] : T(0.f);
+            }
     }
 }
 
@@ -371,7 +388,7 @@ struct Tickets {
 // sums, publishes them, looks back and hands every warp its starting state.
 template <int NS>
 struct Sync {
-    static constexpr int kInfos = NS + 4;  // tile k + NS + 2 is known while k - 1 is finished
+    static constexpr int kInfos = NS <= 4 ? 8 : 16;  // at least NS + 4: tile k + NS + 2 is known while k - 1 is finished
     uint64_t parts[2], ready[2];
     Tile tile[kInfos];
 };
@@ -423,7 +440,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     const int C = p.s.C;
     Tickets tickets(p.ws.ticket, p.tiles);
     auto set_tile = [&](int k, int n) {
-        Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         if (n < p.tiles) t = decode_tile(p.s, n, false);
         else t.tile = -1;
     };
@@ -439,7 +456,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
 
     if (warp == kWarps) {  // the scan warp
         for (int k = 0;; ++k) {
-            const Tile t = sync.tile[k % Sync<NS>::kInfos];
+            const Tile t = sync.tile[k & (Sync<NS>::kInfos - 1)];
             if (t.tile < 0) break;
             int next = 0;
             if (lane == 0) next = tickets.take();
@@ -478,12 +495,12 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     }
 
     auto load = [&](int k) {
-        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         if (t.tile >= 0) {
             typename Plan::Stage &st = sm.stage[k % NS][warp];
-            fill<T, VEC>(st.x, p.x, t, C, warp, lane);
-            fill<T, VEC>(st.r, p.r, t, C, warp, lane);
-            fill<T, VEC>(st.i, p.i, t, C, warp, lane);
+            T *const dst[3] = {st.x, st.r, st.i};
+            const T *const src[3] = {p.x, p.r, p.i};
+            fill<T, VEC, 3>(dst, src, t, C, warp, lane);
         }
         copy_commit();
     };
@@ -492,11 +509,12 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     };
     // the gates of tile k; false when there is none
     auto begin = [&](int k, Held &b) -> bool {
-        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         if (t.tile < 0) return false;
         const int c = t.ct * kGlrCols + 2 * lane;
         const bool a0 = c < C, a1 = c + 1 < C;
         const float2 A = load2<VEC>(p.A + c, a0, a1);
+        const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
         copy_wait<NS - 1>();
         __syncwarp();
@@ -518,9 +536,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
                     if (lane == 0) p.pk.exps[n][row * cols8 + t.ct] = uint8_t(e);
                 }
             }
-            const Gate g = gate(r, i, A);
-            b.e1[j] = g.e1;
-            b.u[j] = income(g, x);
+            token(x, r, i, A, steep, b.e1[j], b.u[j]);
         }
         if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
@@ -539,18 +555,22 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         return true;
     };
     auto finish = [&](int k, const Held &b) {
-        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         const int c = t.ct * kGlrCols + 2 * lane;
         const bool a0 = c < C, a1 = c + 1 < C;
         const int ntok = t.ntok - warp * kTok;
         T *y = p.y + (t.tok + warp * kTok) * C + c;
         tc::mbar_wait(&sync.ready[k & 1], (k >> 1) & 1, p.err);
         float2 h = sm.start[k & 1][warp][lane];
+        auto walk = [&](bool all) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            h = advance(h, b.e1[j], b.u[j]);
-            if (j < ntok) store2<T, VEC>(y + int64_t(j) * C, h, a0, a1);
-        }
+            for (int j = 0; j < kTok; ++j) {
+                h = advance(h, b.e1[j], b.u[j]);
+                if (all || j < ntok) store2<T, VEC>(y + int64_t(j) * C, h, a0, a1);
+            }
+        };
+        if (ntok >= kTok) walk(true);
+        else walk(false);
     };
     for (int k = 0; k < NS; ++k) load(k);
     Held a, b;
@@ -613,7 +633,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
     Tickets tickets(p.ws.ticket, p.tiles);
     auto set_tile = [&](int k, int n) {
-        Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         if (n < p.tiles) t = decode_tile(p.s, n, true);
         else t.tile = -1;
     };
@@ -630,7 +650,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     if (warp == kWarps) {  // the scan warp
         // dA of tile k, which its warps have left by the time they leave the sums of tile k + 2
         auto sum_dA = [&](int k) {
-            const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+            const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
             const int c = t.ct * kGlrCols + 2 * lane;
             float2 sum = sm.dA[k & 1][0][lane];
 #pragma unroll
@@ -639,7 +659,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         };
         int k = 0;
         for (;; ++k) {
-            const Tile t = sync.tile[k % Sync<NS>::kInfos];
+            const Tile t = sync.tile[k & (Sync<NS>::kInfos - 1)];
             if (t.tile < 0) break;
             int next = 0;
             if (lane == 0) next = tickets.take();
@@ -689,12 +709,16 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     }
 
     auto load = [&](int k) {
-        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         if (t.tile >= 0) {
             typename Plan::Stage &st = sm.stage[k % NS][warp];
             if constexpr (PACK) {
-#pragma unroll
-                for (int n = 0; n < 3; ++n) fill<int8_t, VEC>(st.in[n], p.pk.codes[n], t, C, warp, lane);
+                int8_t *const dst[3] = {st.in[0], st.in[1], st.in[2]};
+                const int8_t *const src[3] = {p.pk.codes[0], p.pk.codes[1], p.pk.codes[2]};
+                fill<int8_t, VEC, 3>(dst, src, t, C, warp, lane);
+                T *const ddst[1] = {st.dy};
+                const T *const dsrc[1] = {p.dy};
+                fill<T, VEC, 1>(ddst, dsrc, t, C, warp, lane);
                 // the aligned word around each exponent byte, as far as the array goes
                 if (lane < 3 * kTok) {
                     const int n = lane / kTok, row = warp * kTok + lane % kTok;
@@ -704,11 +728,10 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                     copy_async<4>(&st.exps[n][lane % kTok], e + at, int(all - at < 4 ? all - at : 4));
                 }
             } else {
-                fill<T, VEC>(st.in[0], p.x, t, C, warp, lane);
-                fill<T, VEC>(st.in[1], p.r, t, C, warp, lane);
-                fill<T, VEC>(st.in[2], p.i, t, C, warp, lane);
+                T *const dst[4] = {st.in[0], st.in[1], st.in[2], st.dy};
+                const T *const src[4] = {p.x, p.r, p.i, p.dy};
+                fill<T, VEC, 4>(dst, src, t, C, warp, lane);
             }
-            fill<T, VEC>(st.dy, p.dy, t, C, warp, lane);
         }
         copy_commit();
     };
@@ -728,19 +751,18 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         }
     };
     auto begin = [&](int k, Held &b) -> bool {
-        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         if (t.tile < 0) return false;
         const int c = t.ct * kGlrCols + 2 * lane;
         const float2 A = load2<VEC>(p.A + c, c < C, c + 1 < C);
+        const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;
         copy_wait<NS - 2>();
         __syncwarp();
         const typename Plan::Stage &st = sm.stage[k % NS][warp];
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
-            const Gate g = gate(input(st, t, 1, j), input(st, t, 2, j), A);
-            b.e1[j] = g.e1;
-            b.u[j] = income(g, input(st, t, 0, j));
+            token(input(st, t, 0, j), input(st, t, 1, j), input(st, t, 2, j), A, steep, b.e1[j], b.u[j]);
         }
         if (ntok < kTok) {
 #pragma unroll
@@ -764,7 +786,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         return true;
     };
     auto finish = [&](int k, Held &b) {
-        const Tile &t = sync.tile[k % Sync<NS>::kInfos];
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         const int c = t.ct * kGlrCols + 2 * lane;
         const bool a0 = c < C, a1 = c + 1 < C;
         const float2 A = load2<VEC>(p.A + c, a0, a1);
@@ -774,30 +796,30 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         tc::mbar_wait(&sync.ready[k & 1], (k >> 1) & 1, p.err);
         const float4 s = sm.start[k & 1][warp][lane];
         float2 h = make_float2(s.x, s.y), K = make_float2(s.z, s.w), dA = both(0.f);
-        // u[j] becomes the state before the token
+        // u[j] becomes the state after the token
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            const float2 before = h;
-            h = advance(h, b.e1[j], b.u[j]);
-            b.u[j] = before;
-        }
+        for (int j = 0; j < kTok; ++j) b.u[j] = h = advance(h, b.e1[j], b.u[j]);
+        // a h_{t-1} - a^2 s(i) x / m = h_t - s(i) x / m, as a^2 + m^2 = 1
+        auto walk = [&](bool all) {
 #pragma unroll
-        for (int j = kTok - 1; j >= 0; --j) {
-            if (j >= ntok) continue;
-            const float2 x = input(st, t, 0, j);
-            const Gate g = gate(input(st, t, 1, j), input(st, t, 2, j), A);
-            const float2 rs = make_float2(inv_root(g.w.x), inv_root(g.w.y));
-            const float2 a = add(g.e1, both(1.f)), six = mul(g.si, x);
-            const float2 G = add(K, unpack2(st.dy + j * kGlrCols + 2 * lane));
-            const float2 Gm = mul(mul(G, rs), make_float2(-g.w.x, -g.w.y));
-            const float2 as = mul(mul(a, six), rs);
-            const float2 dl = mul(mul(G, a), add(b.u[j], make_float2(-as.x, -as.y)));
-            dA = fma(dl, g.sr, dA);
-            K = fma(g.e1, G, G);
-            store2<T, VEC>(p.dx + base + int64_t(j) * C, mul(Gm, g.si), a0, a1);
-            store2<T, VEC>(p.di + base + int64_t(j) * C, mul(mul(Gm, six), mul(g.ei, g.si)), a0, a1);
-            store2<T, VEC>(p.dr + base + int64_t(j) * C, mul(mul(dl, g.l), mul(g.er, g.sr)), a0, a1);
-        }
+            for (int j = kTok - 1; j >= 0; --j) {
+                if (!all && j >= ntok) continue;
+                const Sig g = sigmoids(input(st, t, 1, j), input(st, t, 2, j));
+                const float2 w = square_minus_1(b.e1[j]);
+                const float2 rs = make_float2(inv_root(w.x), inv_root(w.y)), six = mul(g.si, input(st, t, 0, j));
+                const float2 G = add(K, unpack2(st.dy + j * kGlrCols + 2 * lane));
+                const float2 Gm = mul(mul(G, rs), make_float2(-w.x, -w.y));
+                const float2 sm_ = mul(six, rs);
+                const float2 dl = mul(G, add(b.u[j], make_float2(-sm_.x, -sm_.y)));
+                dA = fma(dl, g.sr, dA);
+                K = fma(b.e1[j], G, G);
+                store2<T, VEC>(p.dx + base + int64_t(j) * C, mul(Gm, g.si), a0, a1);
+                store2<T, VEC>(p.di + base + int64_t(j) * C, mul(mul(Gm, six), mul(g.ei, g.si)), a0, a1);
+                store2<T, VEC>(p.dr + base + int64_t(j) * C, mul(mul(dl, mul(A, g.sr)), mul(g.er, g.sr)), a0, a1);
+            }
+        };
+        if (ntok >= kTok) walk(true);
+        else walk(false);
         sm.dA[k & 1][warp][lane] = dA;
         __syncwarp();  // this warp's part of the stage is read
         load(k + NS);
@@ -862,8 +884,9 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
             iv = make_float2(to_f32<T>(i[o]), to_f32<T>(i[n]));
             h = make_float2(state[o], state[n]);
         }
-        const Gate g = gate(rv, iv, Av);
-        h = advance(h, g.e1, income(g, xv));
+        float2 e1, u;
+        token(xv, rv, iv, Av, true, e1, u);
+        h = advance(h, e1, u);
         store2<float, VEC>(state + o, h, a0, a1);
         store2<T, VEC>(y + o, h, a0, a1);
     }
