@@ -74,17 +74,22 @@ __device__ __forceinline__ float2 times_plus(float2 a, float2 b, float c) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The two sigmoids.  One reciprocal serves both; the arguments are held at -43 so
-// that the product of the denominators stays finite (s(-43) = 2e-19).
+// e^-v (v held at -43 from below), and s(v) from it; 1 - s(v) = e^-v s(v)
+__device__ __forceinline__ float2 decayed(float2 v) {
+    return make_float2(ex2(max_nan(v.x, -43.f) * -kLog2e), ex2(max_nan(v.y, -43.f) * -kLog2e));
+}
+__device__ __forceinline__ float2 sigmoid(float2 e) {
+    const float2 d = plus(e, 1.f);
+    return make_float2(rcp(d.x), rcp(d.y));
+}
+// The two sigmoids by one reciprocal: with the arguments held at -43 the product of
+// the denominators stays finite (s(-43) = 2e-19).
 struct Sig {
     float2 sr, si;  // s(r), s(i)
-    float2 er, ei;  // e^-r, e^-i: 1 - s(r) = er * sr
 };
 __device__ __forceinline__ Sig sigmoids(float2 r, float2 i) {
     Sig g;
-    g.er = make_float2(ex2(max_nan(r.x, -43.f) * -kLog2e), ex2(max_nan(r.y, -43.f) * -kLog2e));
-    g.ei = make_float2(ex2(max_nan(i.x, -43.f) * -kLog2e), ex2(max_nan(i.y, -43.f) * -kLog2e));
-    const float2 dr = plus(g.er, 1.f), di = plus(g.ei, 1.f);
+    const float2 dr = plus(decayed(r), 1.f), di = plus(decayed(i), 1.f);
     const float2 d = mul(dr, di), q = make_float2(rcp(d.x), rcp(d.y));
     g.sr = mul(di, q);
     g.si = mul(dr, q);
@@ -167,6 +172,17 @@ __device__ __forceinline__ void store_code2(int8_t *p, int c0, int c1, bool a0, 
     }
 }
 
+// A warp's 64 values of one row into the n-th checkpoint: one block of it.
+template <bool VEC>
+__device__ __forceinline__ void pack_row(const GlrPacked &pk, int n, float2 v, int64_t at, int64_t block, int lane,
+                                         int c, int C) {
+    const uint32_t e = pack8_exp(__reduce_max_sync(
+        0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)));
+    const float inv = pack8_inv(e);
+    store_code2<VEC>(pk.codes[n] + at, pack8_code(v.x, inv), pack8_code(v.y, inv), c < C, c + 1 < C);
+    if (lane == 0) pk.exps[n][block] = uint8_t(e);
+}
+
 // ---------------------------------------------------------------------------
 // shared memory: a ring of stages, each the raw values of one tile
 // ---------------------------------------------------------------------------
@@ -196,22 +212,38 @@ struct Tile {
     int stride;    // the previous one of the chain is tile - stride
     int row;       // row of the states
     bool first, last;  // the sequence's first / last chunk
+    bool full;     // 64 tokens of 64 channels
     int64_t tok;   // first token (row * T + offset)
+    int64_t base;  // its first value in a [tokens, C] array
     int64_t chunk; // row of chunk_states
+};
+
+// n / d by a multiplication (Granlund and Montgomery): n < 2^31, 0 < d < 2^31.
+struct Divide {
+    uint32_t d, m, s;
+    static Divide by(uint32_t d) {
+        uint32_t s = 0;
+        while ((uint64_t(1) << s) < d) ++s;
+        return Divide{d, uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1), s};
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
+struct TileDivide {
+    Divide nct, batch;
 };
 
 // Tickets run over the channel tiles fastest, then over the chains, then along
 // them (against time for the backward pass).
-__device__ __forceinline__ Tile decode_tile(const GlrShape &s, int tile, bool reverse) {
+__device__ __forceinline__ Tile decode_tile(const GlrShape &s, const TileDivide &dv, int tile, bool reverse) {
     Tile t;
     t.tile = tile;
-    t.ct = tile % s.nct;
-    int g = tile / s.nct;
+    int g = int(dv.nct(uint32_t(tile)));
+    t.ct = tile - g * s.nct;
     int k, nc;
     if (s.nseq == 0) {
         nc = s.nc;
-        t.row = g % s.batch;
-        k = g / s.batch;
+        k = int(dv.batch(uint32_t(g)));
+        t.row = g - k * s.batch;
         if (reverse) k = nc - 1 - k;
         t.stride = s.batch * s.nct;
         t.tok = int64_t(t.row) * s.T + int64_t(k) * kGlrChunk;
@@ -234,6 +266,8 @@ __device__ __forceinline__ Tile decode_tile(const GlrShape &s, int tile, bool re
     }
     t.first = k == 0;
     t.last = k == nc - 1;
+    t.full = t.ntok == kGlrChunk && (t.ct + 1) * kGlrCols <= s.C;
+    t.base = t.tok * s.C + t.ct * kGlrCols;
     t.rank = reverse ? nc - 1 - k : k;
     return t;
 }
@@ -277,14 +311,16 @@ __device__ __forceinline__ bool set(float2 v) { return set(v.x) && set(v.y); }
 __device__ __forceinline__ bool set(float4 v) { return set(v.x) && set(v.y) && set(v.z) && set(v.w); }
 
 constexpr int kWindow = 16;  // predecessors that a tile looks back over
-constexpr int kBatch = 4;    // sums fetched at a time
+constexpr int kBatch = 8;    // sums fetched at a time
 
 // The state that enters the tile, for one warp (t.rank > 0): the outgoing state of
 // the nearest predecessor that has published it, taken through the sums of those
-// in between, in their order.  Lanes 0 .. 15 watch the predecessors' states,
-// lanes 16 .. 31 their sums.  Gives up with the error word set after kWaitLimitNs.
+// in between, in their order.  `h` comes in as get_state() of the tile before,
+// fetched ahead.  Otherwise lanes 0 .. 15 watch the predecessors' states, lanes
+// 16 .. 31 their sums.  Gives up with the error word set after kWaitLimitNs.
 __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, int lane, float2 &h,
                                           unsigned int *err) {
+    if (__all_sync(0xffffffffu, set(h))) return true;
     const int window = min(t.rank, kWindow), mine = lane % kWindow;
     const int64_t watched = (t.tile - int64_t(mine + 1) * t.stride) * 32;
     const void *f = lane < kWindow ? static_cast<const void *>(ws.state + watched)
@@ -330,7 +366,7 @@ __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, i
 }
 
 constexpr int kWarps = 8;                     // compute warps of a tile
-constexpr int kThreads = 32 * (kWarps + 1);   // and the scan warp
+constexpr int kGroupThreads = 32 * (kWarps + 1);  // and the scan warp
 constexpr int kTok = kGlrChunk / kWarps;      // tokens of a warp
 constexpr int kWarpVals = kTok * kGlrCols;
 
@@ -340,13 +376,20 @@ template <typename T, bool VEC, int N>
 __device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N], const Tile &t, int C, int warp,
                                      int lane) {
     const int c0 = t.ct * kGlrCols, ntok = t.ntok - warp * kTok;
-    const int64_t tok = t.tok + warp * kTok;
     if (VEC) {
         constexpr int kBytes = sizeof(T) == 1 ? 8 : 16, kVals = kBytes / sizeof(T), kRow = kGlrCols / kVals;
         constexpr int kRows = 32 / kRow;  // tokens of one step
         const int row = lane / kRow, v = (lane % kRow) * kVals;
+        int64_t o = t.base + (int64_t(warp * kTok + row) * C + v);
+        if (t.full) {
+#pragma unroll
+            for (int n = 0; n < kTok / kRows; ++n, o += int64_t(kRows) * C)
+#pragma unroll
+                for (int a = 0; a < N; ++a)
+                    copy_async<kBytes>(dst[a] + n * kRows * kGlrCols + lane * kVals, src[a] + o, kBytes);
+            return;
+        }
         const bool in = c0 + v < C;
-        int64_t o = (tok + row) * C + c0 + v;
 #pragma unroll
         for (int n = 0; n < kTok / kRows; ++n, o += int64_t(kRows) * C) {
             const bool ok = in && row + n * kRows < ntok;
@@ -360,7 +403,7 @@ __device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N
 #pragma unroll 8
             for (int n = 0; n < kWarpVals / 32; ++n) {
                 const int id = n * 32 + lane, row = id / kGlrCols, v = id % kGlrCols;
-                dst[a][id] = row < ntok && c0 + v < C ? src[a][(tok + row) * C + c0 + v] : T(0.f);
+                dst[a][id] = row < ntok && c0 + v < C ? src[a][t.base + int64_t(warp * kTok + row) * C + v] : T(0.f);
             }
     }
 }
@@ -368,28 +411,42 @@ __device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N
 // Tiles by ticket, or strided over the grid where no state is handed on.
 struct Tickets {
     unsigned int *ticket;
-    int tiles, mine;
-    __device__ __forceinline__ Tickets(unsigned int *t, int n) : ticket(t), tiles(n), mine(blockIdx.x) {}
-    __device__ __forceinline__ int take() {
-        if (ticket) return int(min(atomicAdd(ticket, 1u) + 1u, 0x7fffffffu));  // it starts at all ones
+    int tiles, mine, step;
+    __device__ __forceinline__ Tickets(unsigned int *t, int n, int groups, int group)
+        : ticket(t), tiles(n), mine(group * gridDim.x + blockIdx.x), step(groups * gridDim.x) {}
+    // The next tile, raw: what atomicAdd returned, whose first use waits for it.
+    __device__ __forceinline__ uint32_t take() {
+        if (ticket) return atomicAdd(ticket, 1u);
         const int n = mine;
-        mine = mine > tiles ? mine : mine + int(gridDim.x);
-        return n;
+        mine = mine > tiles ? mine : mine + step;
+        return uint32_t(n) - 1u;
     }
+    // The ticket word starts at all ones, so a raw ticket is one less than its tile.
+    static __device__ __forceinline__ int tile_of(uint32_t raw) { return int(min(raw + 1u, 0x7fffffffu)); }
 };
 
 // ---------------------------------------------------------------------------
-// a block: compute warps, which never wait for one another, and a scan warp
+// a group: compute warps, which never wait for one another, and a scan warp
 // ---------------------------------------------------------------------------
-// Each compute warp copies, reads and writes its own eight tokens of every tile,
-// and two tiles are under way: it forms the gates of tile k, leaves their
-// products and sums, and then finishes tile k - 1 from the state that the scan
-// warp has found meanwhile.  The scan warp takes the tickets, joins the warps'
-// sums, publishes them, looks back and hands every warp its starting state.
+// Each compute warp copies, reads and writes its own eight tokens of every tile:
+// it forms their gates, leaves their product and sum, and finishes the tokens
+// once it has the state before them.  The scan warp takes the tickets, joins the
+// warps' sums, publishes them, looks back and hands every warp its start.  One
+// block an SM holds three such groups, which share nothing, so that two of them
+// compute while one waits for its state.
+//
+// Registers decide the shape: 27 warps leave 72 a thread, enough for a tile's
+// gates and no more.  Two groups that held two tiles each, to bridge the wait
+// themselves, spilled; next to this much shared memory L1 holds no spilled
+// words, and the backward pass took half as long again.
+constexpr int kGroups = 3;
+constexpr int kBlock = kGroups * kGroupThreads;
+
 template <int NS>
 struct Sync {
-    static constexpr int kInfos = NS <= 4 ? 8 : 16;  // at least NS + 4: tile k + NS + 2 is known while k - 1 is finished
-    uint64_t parts[2], ready[2];
+    // tile k + NS + 1 is known when tile k is finished
+    static constexpr int kInfos = NS <= 2 ? 4 : 8;
+    uint64_t parts, ready;
     Tile tile[kInfos];
 };
 __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
@@ -411,85 +468,92 @@ struct FwdArgs {
     GlrPacked pk;
     unsigned int *err;
     int tiles;
+    TileDivide dv;
 };
 template <typename T>
 struct FwdPlan {
-    static constexpr int kStages = sizeof(T) == 2 ? 3 : 2;
-    static constexpr int kPerSm = 2;
+    static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
     struct Stage {
         T x[kWarpVals], r[kWarpVals], i[kWarpVals];
     };
-    struct Smem {
+    struct alignas(128) Smem {
         Stage stage[kStages][kWarps];
-        float4 part[2][kWarps][32];  // products and sums of the warps' tokens
-        float2 start[2][kWarps][32];  // the states before them
+        // products and sums of the warps' tokens; in their place then the states before them
+        float4 part[kWarps][32];
         Sync<kStages> sync;
     };
-    static constexpr int smem = sizeof(Smem);
+    static constexpr int smem = kGroups * sizeof(Smem);
+    static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
 };
 
 template <typename T, bool VEC, bool PACK>
-__global__ void __launch_bounds__(kThreads, FwdPlan<T>::kPerSm)
+__global__ void __launch_bounds__(kBlock, 1)
 glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     using Plan = FwdPlan<T>;
     constexpr int NS = Plan::kStages;
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    typename Plan::Smem &sm = *reinterpret_cast<typename Plan::Smem *>(smem_raw);
+    const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
+    typename Plan::Smem &sm = reinterpret_cast<typename Plan::Smem *>(smem_raw)[group];
     Sync<NS> &sync = sm.sync;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = p.s.C;
-    Tickets tickets(p.ws.ticket, p.tiles);
-    auto set_tile = [&](int k, int n) {
+    Tickets tickets(p.ws.ticket, p.tiles, kGroups, group);
+    auto set_tile = [&](int k, uint32_t raw) {
+        const int n = Tickets::tile_of(raw);
         Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
-        if (n < p.tiles) t = decode_tile(p.s, n, false);
+        if (n < p.tiles) t = decode_tile(p.s, p.dv, n, false);
         else t.tile = -1;
     };
-    if (threadIdx.x == kWarps * 32) {
-        for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(&sync.parts[b], kWarps);
-            tc::mbar_init(&sync.ready[b], 1);
-        }
+    if (warp == kWarps && lane == 0) {
+        tc::mbar_init(&sync.parts, kWarps);
+        tc::mbar_init(&sync.ready, 1);
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
     if (warp == kWarps) {  // the scan warp
+        uint32_t next = 0;  // a ticket taken one tile ago
+        if (lane == 0) next = tickets.take();
         for (int k = 0;; ++k) {
             const Tile t = sync.tile[k & (Sync<NS>::kInfos - 1)];
             if (t.tile < 0) break;
-            int next = 0;
-            if (lane == 0) next = tickets.take();
+            uint32_t later = 0;
+            if (lane == 0) later = tickets.take();
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = both(0.f);
             if (t.first && p.h0) h = load2<VEC>(p.h0 + int64_t(t.row) * C + c, a0, a1);
-            tc::mbar_wait(&sync.parts[k & 1], (k >> 1) & 1, p.err);
-            float4 q[kWarps];
+            tc::mbar_wait(&sync.parts, k & 1, p.err);
+            float2 P = both(1.f), S = both(0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) q[w] = sm.part[k & 1][w][lane];
-            float2 P = make_float2(q[0].x, q[0].y), S = make_float2(q[0].z, q[0].w);
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const float2 d = make_float2(q[w].x, q[w].y);
-                P = mul(P, d);
-                S = fma(d, S, make_float2(q[w].z, q[w].w));
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 q = sm.part[w][lane];
+                P = mul(P, make_float2(q.x, q.y));
+                S = fma(make_float2(q.x, q.y), S, make_float2(q.z, q.w));
             }
             if (!t.first) {
                 if (!t.last) put_sums(p.ws, t.tile, lane, P, S);
-                look_back(p.ws, t, lane, h, p.err);
+                h = get_state(p.ws, t.tile - int64_t(t.stride), lane);
             }
+            if (lane == 0) {  // while the state is on its way
+                set_tile(k + NS + 1, next);
+                next = later;
+            }
+            __syncwarp();
+            if (!t.first) look_back(p.ws, t, lane, h, p.err);
             const float2 out = fma(P, h, S);
             if (!t.last) put_state(p.ws, t.tile, lane, out);
-            if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, h, a0, a1);
-            if (t.last && p.fin) store2<float, VEC>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
+            const float2 start = h;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                sm.start[k & 1][w][lane] = h;
-                h = fma(make_float2(q[w].x, q[w].y), h, make_float2(q[w].z, q[w].w));
+                const float4 q = sm.part[w][lane];
+                *reinterpret_cast<float2 *>(&sm.part[w][lane]) = h;
+                h = fma(make_float2(q.x, q.y), h, make_float2(q.z, q.w));
             }
-            if (lane == 0) set_tile(k + NS + 2, next);
-            arrive_warp(&sync.ready[k & 1], lane);
+            arrive_warp(&sync.ready, lane);
+            if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, start, a0, a1);
+            if (t.last && p.fin) store2<float, VEC>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
         }
         return;
     }
@@ -504,83 +568,70 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         }
         copy_commit();
     };
-    struct Held {
-        float2 e1[kTok], u[kTok];
-    };
-    // the gates of tile k; false when there is none
-    auto begin = [&](int k, Held &b) -> bool {
+    auto rates = [&](int k) -> float2 {  // A of tile k
         const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
-        if (t.tile < 0) return false;
         const int c = t.ct * kGlrCols + 2 * lane;
-        const bool a0 = c < C, a1 = c + 1 < C;
-        const float2 A = load2<VEC>(p.A + c, a0, a1);
+        return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
+    };
+    for (int k = 0; k < NS; ++k) load(k);
+    float2 A = rates(0);
+    for (int k = 0;; ++k) {
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        if (t.tile < 0) break;
         const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
         copy_wait<NS - 1>();
         __syncwarp();
         const typename Plan::Stage &st = sm.stage[k % NS][warp];
+        if (PACK) {
+            const int c = t.ct * kGlrCols + 2 * lane;
+            const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
+            int64_t row = t.tok + warp * kTok, o = t.base + (int64_t(warp * kTok) * C + 2 * lane);
+#pragma unroll
+            for (int j = 0; j < kTok; ++j, ++row, o += C) {
+                if (j >= ntok) break;
+                pack_row<VEC>(p.pk, 0, unpack2(st.x + j * kGlrCols + 2 * lane), o, row * cols8 + t.ct, lane, c, C);
+                pack_row<VEC>(p.pk, 1, unpack2(st.r + j * kGlrCols + 2 * lane), o, row * cols8 + t.ct, lane, c, C);
+                pack_row<VEC>(p.pk, 2, unpack2(st.i + j * kGlrCols + 2 * lane), o, row * cols8 + t.ct, lane, c, C);
+            }
+        }
+        float2 e1[kTok], u[kTok], P = both(1.f), S = both(0.f);
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
             const int o = j * kGlrCols + 2 * lane;
-            const float2 x = unpack2(st.x + o), r = unpack2(st.r + o), i = unpack2(st.i + o);
-            if (PACK && j < ntok) {
-                const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock, row = t.tok + warp * kTok + j;
-#pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    const float2 v = n == 0 ? x : n == 1 ? r : i;
-                    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu,
-                                                                          __float_as_uint(v.y) & 0x7fffffffu));
-                    const uint32_t e = pack8_exp(m);
-                    const float inv = pack8_inv(e);
-                    store_code2<VEC>(p.pk.codes[n] + row * C + c, pack8_code(v.x, inv), pack8_code(v.y, inv), a0, a1);
-                    if (lane == 0) p.pk.exps[n][row * cols8 + t.ct] = uint8_t(e);
-                }
-            }
-            token(x, r, i, A, steep, b.e1[j], b.u[j]);
+            token(unpack2(st.x + o), unpack2(st.r + o), unpack2(st.i + o), A, steep, e1[j], u[j]);
         }
         if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
             for (int j = 0; j < kTok; ++j)
-                if (j >= ntok) b.e1[j] = b.u[j] = both(0.f);
+                if (j >= ntok) e1[j] = u[j] = both(0.f);
         }
-        float2 P = both(1.f), S = both(0.f);
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
-            P = fma(b.e1[j], P, P);
-            S = advance(S, b.e1[j], b.u[j]);
+            P = fma(e1[j], P, P);
+            S = advance(S, e1[j], u[j]);
         }
-        sm.part[k & 1][warp][lane] = make_float4(P.x, P.y, S.x, S.y);
-        arrive_warp(&sync.parts[k & 1], lane);  // and this warp's part of the stage is read
+        sm.part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+        arrive_warp(&sync.parts, lane);  // and this warp's part of the stage is read
         load(k + NS);
-        return true;
-    };
-    auto finish = [&](int k, const Held &b) {
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
-        const int c = t.ct * kGlrCols + 2 * lane;
-        const bool a0 = c < C, a1 = c + 1 < C;
-        const int ntok = t.ntok - warp * kTok;
-        T *y = p.y + (t.tok + warp * kTok) * C + c;
-        tc::mbar_wait(&sync.ready[k & 1], (k >> 1) & 1, p.err);
-        float2 h = sm.start[k & 1][warp][lane];
-        auto walk = [&](bool all) {
+        A = rates(k + 1);
+        T *y = p.y + (t.base + (int64_t(warp * kTok) * C + 2 * lane));
+        tc::mbar_wait(&sync.ready, k & 1, p.err);
+        float2 h = *reinterpret_cast<const float2 *>(&sm.part[warp][lane]);
+        if (t.full) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                h = advance(h, b.e1[j], b.u[j]);
-                if (all || j < ntok) store2<T, VEC>(y + int64_t(j) * C, h, a0, a1);
+            for (int j = 0; j < kTok; ++j, y += C) {
+                h = advance(h, e1[j], u[j]);
+                store2<T, VEC>(y, h, true, true);
             }
-        };
-        if (ntok >= kTok) walk(true);
-        else walk(false);
-    };
-    for (int k = 0; k < NS; ++k) load(k);
-    Held a, b;
-    for (int k = 0;; k += 2) {
-        const bool more = begin(k, a);
-        if (k > 0) finish(k - 1, b);
-        if (!more) break;
-        const bool again = begin(k + 1, b);
-        finish(k, a);
-        if (!again) break;
+        } else {
+            const int c = t.ct * kGlrCols + 2 * lane;
+#pragma unroll
+            for (int j = 0; j < kTok; ++j, y += C) {
+                h = advance(h, e1[j], u[j]);
+                if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C);
+            }
+        }
     }
 }
 
@@ -598,112 +649,121 @@ struct BwdArgs {
     float *dinit, *dA_part;
     unsigned int *err;
     int tiles;
+    TileDivide dv;
 };
 template <typename T, bool PACK>
 struct BwdPlan {
-    static constexpr int kStages = 3;  // two tiles under way, one on the way
-    static constexpr int kPerSm = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int kStages = sizeof(T) == 2 ? (PACK ? 3 : 2) : (PACK ? 2 : 1);
     using In = std::conditional_t<PACK, int8_t, T>;
     struct Stage {
         In in[3][kWarpVals];
         T dy[kWarpVals];
-        uint32_t exps[PACK ? 3 : 1][kTok];  // the words that hold the exponent bytes
+        uint32_t exps[PACK ? 3 : 1][PACK ? kTok : 4];  // the words that hold the exponent bytes
     };
-    struct Smem {
+    struct alignas(128) Smem {
         Stage stage[kStages][kWarps];
-        float4 part[2][kWarps][32];   // products, forward sums
-        float2 rpart[2][kWarps][32];  // reverse sums
-        float2 dA[2][kWarps][32];
-        float4 start[2][kWarps][32];  // the state before the warp's tokens, K behind them
+        // products and forward sums; in their place then the state before the warp's
+        // tokens and K behind them
+        float4 part[kWarps][32];
+        float2 rpart[kWarps][32];  // reverse sums
+        float2 dA[kWarps][32];
         Sync<kStages> sync;
     };
-    static constexpr int smem = sizeof(Smem);
+    static constexpr int smem = kGroups * sizeof(Smem);
+    static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
 };
 
 template <typename T, bool VEC, bool PACK>
-__global__ void __launch_bounds__(kThreads, BwdPlan<T, PACK>::kPerSm)
+__global__ void __launch_bounds__(kBlock, 1)
 glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     using Plan = BwdPlan<T, PACK>;
+    using In = typename Plan::In;
     constexpr int NS = Plan::kStages;
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    typename Plan::Smem &sm = *reinterpret_cast<typename Plan::Smem *>(smem_raw);
+    const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
+    typename Plan::Smem &sm = reinterpret_cast<typename Plan::Smem *>(smem_raw)[group];
     Sync<NS> &sync = sm.sync;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int C = p.s.C;
     const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
-    Tickets tickets(p.ws.ticket, p.tiles);
-    auto set_tile = [&](int k, int n) {
+    Tickets tickets(p.ws.ticket, p.tiles, kGroups, group);
+    auto set_tile = [&](int k, uint32_t raw) {
+        const int n = Tickets::tile_of(raw);
         Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
-        if (n < p.tiles) t = decode_tile(p.s, n, true);
+        if (n < p.tiles) t = decode_tile(p.s, p.dv, n, true);
         else t.tile = -1;
     };
-    if (threadIdx.x == kWarps * 32) {
-        for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(&sync.parts[b], kWarps);
-            tc::mbar_init(&sync.ready[b], 1);
-        }
+    if (warp == kWarps && lane == 0) {
+        tc::mbar_init(&sync.parts, kWarps);
+        tc::mbar_init(&sync.ready, 1);
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
     if (warp == kWarps) {  // the scan warp
-        // dA of tile k, which its warps have left by the time they leave the sums of tile k + 2
+        // dA of tile k, which its warps have left by the time they leave the sums of tile k + 1
         auto sum_dA = [&](int k) {
             const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
             const int c = t.ct * kGlrCols + 2 * lane;
-            float2 sum = sm.dA[k & 1][0][lane];
+            float2 sum = sm.dA[0][lane];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[k & 1][w][lane]);
+            for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[w][lane]);
             store2<float, VEC>(p.dA_part + t.chunk * C + c, sum, c < C, c + 1 < C);
         };
+        uint32_t next = 0;  // a ticket taken one tile ago
+        if (lane == 0) next = tickets.take();
         int k = 0;
         for (;; ++k) {
             const Tile t = sync.tile[k & (Sync<NS>::kInfos - 1)];
             if (t.tile < 0) break;
-            int next = 0;
-            if (lane == 0) next = tickets.take();
+            uint32_t later = 0;
+            if (lane == 0) later = tickets.take();
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = load2<VEC>(p.states + t.chunk * C + c, a0, a1), K = both(0.f);
             if (t.last && p.dfin) K = load2<VEC>(p.dfin + int64_t(t.row) * C + c, a0, a1);
-            tc::mbar_wait(&sync.parts[k & 1], (k >> 1) & 1, p.err);
-            float2 q[kWarps], z[kWarps];
+            tc::mbar_wait(&sync.parts, k & 1, p.err);
+            float2 P = both(1.f), R = both(0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 v = sm.part[k & 1][w][lane];
-                q[w] = make_float2(v.x, v.y);
-                z[w] = sm.rpart[k & 1][w][lane];
-                *reinterpret_cast<float2 *>(&sm.start[k & 1][w][lane]) = h;
-                h = fma(q[w], h, make_float2(v.z, v.w));
-            }
-            float2 P = q[kWarps - 1], R = z[kWarps - 1];
-#pragma unroll
-            for (int w = kWarps - 2; w >= 0; --w) {
-                P = mul(P, q[w]);
-                R = fma(q[w], R, z[w]);
+            for (int w = kWarps - 1; w >= 0; --w) {
+                const float2 q = *reinterpret_cast<const float2 *>(&sm.part[w][lane]);
+                P = mul(P, q);
+                R = fma(q, R, sm.rpart[w][lane]);
             }
             if (!t.last) {
                 if (!t.first) put_sums(p.ws, t.tile, lane, P, R);
-                look_back(p.ws, t, lane, K, p.err);
+                K = get_state(p.ws, t.tile - int64_t(t.stride), lane);
             }
+            if (k >= 1) sum_dA(k - 1);
+            __syncwarp();
+            if (lane == 0) {  // while K is on its way
+                set_tile(k + NS + 1, next);
+                next = later;
+            }
+            __syncwarp();
+            if (!t.last) look_back(p.ws, t, lane, K, p.err);
             const float2 out = fma(P, K, R);
             if (!t.first) put_state(p.ws, t.tile, lane, out);
             if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
+            float2 q[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 v = sm.part[w][lane];
+                q[w] = make_float2(v.x, v.y);
+                *reinterpret_cast<float2 *>(&sm.part[w][lane]) = h;
+                h = fma(q[w], h, make_float2(v.z, v.w));
+            }
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
-                reinterpret_cast<float2 *>(&sm.start[k & 1][w][lane])[1] = K;
-                K = fma(q[w], K, z[w]);
+                reinterpret_cast<float2 *>(&sm.part[w][lane])[1] = K;
+                K = fma(q[w], K, sm.rpart[w][lane]);
             }
-            if (k >= 2) sum_dA(k - 2);
-            __syncwarp();
-            if (lane == 0) set_tile(k + NS + 2, next);
-            arrive_warp(&sync.ready[k & 1], lane);
+            arrive_warp(&sync.ready, lane);
         }
-        // the last two tiles: their warps say when they are through
-        for (int j = k < 2 ? 0 : k - 2; j < k; ++j) {
-            tc::mbar_wait(&sync.parts[(j + 2) & 1], ((j + 2) >> 1) & 1, p.err);
-            sum_dA(j);
+        if (k > 0) {  // the last tile: its warps say when they are through
+            tc::mbar_wait(&sync.parts, k & 1, p.err);
+            sum_dA(k - 1);
         }
         return;
     }
@@ -735,111 +795,104 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         }
         copy_commit();
     };
-    struct Held {
-        float2 e1[kTok], u[kTok];
-    };
-    // x, r or i of token j of this warp
-    auto input = [&](const typename Plan::Stage &st, const Tile &t, int n, int j) -> float2 {
-        const int o = j * kGlrCols + 2 * lane;
-        if constexpr (PACK) {
-            const uint32_t shift = 8 * uint32_t(((t.tok + warp * kTok + j) * cols8 + t.ct) & 3);
-            const float step = pack8_step((st.exps[n][j] >> shift) & 255u);
-            const char2 q = *reinterpret_cast<const char2 *>(st.in[n] + o);
-            return make_float2(float(q.x) * step, float(q.y) * step);
-        } else {
-            return unpack2(st.in[n] + o);
-        }
-    };
-    auto begin = [&](int k, Held &b) -> bool {
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
-        if (t.tile < 0) return false;
-        const int c = t.ct * kGlrCols + 2 * lane;
-        const float2 A = load2<VEC>(p.A + c, c < C, c + 1 < C);
-        const bool steep = steep_warp(A);
-        const int ntok = t.ntok - warp * kTok;
-        copy_wait<NS - 2>();
-        __syncwarp();
-        const typename Plan::Stage &st = sm.stage[k % NS][warp];
-#pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            token(input(st, t, 0, j), input(st, t, 1, j), input(st, t, 2, j), A, steep, b.e1[j], b.u[j]);
-        }
-        if (ntok < kTok) {
-#pragma unroll
-            for (int j = 0; j < kTok; ++j)
-                if (j >= ntok) b.e1[j] = b.u[j] = both(0.f);
-        }
-        float2 P = both(1.f), S = both(0.f), R = both(0.f);
-#pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            P = fma(b.e1[j], P, P);
-            S = advance(S, b.e1[j], b.u[j]);
-        }
-#pragma unroll
-        for (int j = kTok - 1; j >= 0; --j) {
-            R = add(R, unpack2(st.dy + j * kGlrCols + 2 * lane));  // 0 behind the end
-            R = fma(b.e1[j], R, R);
-        }
-        sm.part[k & 1][warp][lane] = make_float4(P.x, P.y, S.x, S.y);
-        sm.rpart[k & 1][warp][lane] = R;
-        arrive_warp(&sync.parts[k & 1], lane);
-        return true;
-    };
-    auto finish = [&](int k, Held &b) {
+    auto rates = [&](int k) -> float2 {  // A of tile k
         const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
         const int c = t.ct * kGlrCols + 2 * lane;
-        const bool a0 = c < C, a1 = c + 1 < C;
-        const float2 A = load2<VEC>(p.A + c, a0, a1);
-        const int ntok = t.ntok - warp * kTok;
-        const int64_t base = (t.tok + warp * kTok) * C + c;
-        const typename Plan::Stage &st = sm.stage[k % NS][warp];
-        tc::mbar_wait(&sync.ready[k & 1], (k >> 1) & 1, p.err);
-        const float4 s = sm.start[k & 1][warp][lane];
-        float2 h = make_float2(s.x, s.y), K = make_float2(s.z, s.w), dA = both(0.f);
-        // u[j] becomes the state after the token
-#pragma unroll
-        for (int j = 0; j < kTok; ++j) b.u[j] = h = advance(h, b.e1[j], b.u[j]);
-        // a h_{t-1} - a^2 s(i) x / m = h_t - s(i) x / m, as a^2 + m^2 = 1
-        auto walk = [&](bool all) {
-#pragma unroll
-            for (int j = kTok - 1; j >= 0; --j) {
-                if (!all && j >= ntok) continue;
-                const Sig g = sigmoids(input(st, t, 1, j), input(st, t, 2, j));
-                const float2 w = square_minus_1(b.e1[j]);
-                const float2 rs = make_float2(inv_root(w.x), inv_root(w.y)), six = mul(g.si, input(st, t, 0, j));
-                const float2 G = add(K, unpack2(st.dy + j * kGlrCols + 2 * lane));
-                const float2 Gm = mul(mul(G, rs), make_float2(-w.x, -w.y));
-                const float2 sm_ = mul(six, rs);
-                const float2 dl = mul(G, add(b.u[j], make_float2(-sm_.x, -sm_.y)));
-                dA = fma(dl, g.sr, dA);
-                K = fma(b.e1[j], G, G);
-                store2<T, VEC>(p.dx + base + int64_t(j) * C, mul(Gm, g.si), a0, a1);
-                store2<T, VEC>(p.di + base + int64_t(j) * C, mul(mul(Gm, six), mul(g.ei, g.si)), a0, a1);
-                store2<T, VEC>(p.dr + base + int64_t(j) * C, mul(mul(dl, mul(A, g.sr)), mul(g.er, g.sr)), a0, a1);
-            }
-        };
-        if (ntok >= kTok) walk(true);
-        else walk(false);
-        sm.dA[k & 1][warp][lane] = dA;
-        __syncwarp();  // this warp's part of the stage is read
-        load(k + NS);
+        return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
     for (int k = 0; k < NS; ++k) load(k);
-    Held a, b;
+    float2 A = rates(0);
     int k = 0;
-    for (;; k += 2) {
-        const bool more = begin(k, a);
-        if (k > 0) finish(k - 1, b);
-        if (!more) break;
-        const bool again = begin(k + 1, b);
-        finish(k, a);
-        if (!again) {
-            ++k;
-            break;
+    for (;; ++k) {
+        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        if (t.tile < 0) break;
+        const bool steep = steep_warp(A);
+        const int ntok = t.ntok - warp * kTok;
+        copy_wait<NS - 1>();
+        __syncwarp();
+        const typename Plan::Stage &st = sm.stage[k % NS][warp];
+        // x, r or i of token j of this warp
+        auto input = [&](int n, int j) -> float2 {
+            const int o = j * kGlrCols + 2 * lane;
+            if constexpr (PACK) {
+                const uint32_t shift = 8 * uint32_t(((t.tok + warp * kTok + j) * cols8 + t.ct) & 3);
+                const float step = pack8_step((st.exps[n][j] >> shift) & 255u);
+                const char2 q = *reinterpret_cast<const char2 *>(st.in[n] + o);
+                return make_float2(float(q.x) * step, float(q.y) * step);
+            } else {
+                return unpack2(st.in[n] + o);
+            }
+        };
+        auto cotangent = [&](int j) -> float2 { return unpack2(st.dy + j * kGlrCols + 2 * lane); };
+        float2 e1[kTok], u[kTok];
+        {
+            float2 P = both(1.f), S = both(0.f), R = both(0.f);
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) token(input(0, j), input(1, j), input(2, j), A, steep, e1[j], u[j]);
+            if (ntok < kTok) {  // behind the sequence's end: the identity
+#pragma unroll
+                for (int j = 0; j < kTok; ++j)
+                    if (j >= ntok) e1[j] = u[j] = both(0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) {
+                P = fma(e1[j], P, P);
+                S = advance(S, e1[j], u[j]);
+            }
+#pragma unroll
+            for (int j = kTok - 1; j >= 0; --j) {
+                R = add(R, cotangent(j));  // 0 behind the end
+                R = fma(e1[j], R, R);
+            }
+            sm.part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+            sm.rpart[warp][lane] = R;
         }
+        arrive_warp(&sync.parts, lane);
+        tc::mbar_wait(&sync.ready, k & 1, p.err);
+        const float4 s = sm.part[warp][lane];
+        float2 K = make_float2(s.z, s.w), dA = both(0.f);
+        {
+            // u[j] becomes the state before the token
+            float2 h = make_float2(s.x, s.y);
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) {
+                const float2 before = h;
+                h = advance(h, e1[j], u[j]);
+                u[j] = before;
+            }
+        }
+        int64_t o = t.base + (int64_t(warp * kTok + kTok - 1) * C + 2 * lane);
+        const int c = t.ct * kGlrCols + 2 * lane;
+        const bool a0 = c < C, a1 = c + 1 < C;
+        auto walk = [&](bool all) {
+#pragma unroll
+            for (int j = kTok - 1; j >= 0; --j, o -= C) {
+                if (!all && j >= ntok) continue;
+                const float2 er = decayed(input(1, j)), ei = decayed(input(2, j));
+                const float2 dr = plus(er, 1.f), di = plus(ei, 1.f), d = mul(dr, di);
+                const float2 q = make_float2(rcp(d.x), rcp(d.y)), sr = mul(di, q), si = mul(dr, q);
+                const float2 w = square_minus_1(e1[j]), rs = make_float2(inv_root(w.x), inv_root(w.y));
+                const float2 m = mul(make_float2(-w.x, -w.y), rs), a = plus(e1[j], 1.f), six = mul(si, input(0, j));
+                const float2 G = add(K, cotangent(j)), Gm = mul(G, m);
+                // (G (h_t - s(i) x / m) would do, as a^2 + m^2 = 1, but for a small a it is
+                // the difference of two numbers that are almost the same)
+                const float2 as = mul(mul(a, six), rs);
+                const float2 dl = mul(mul(G, a), add(u[j], make_float2(-as.x, -as.y)));
+                dA = fma(dl, sr, dA);
+                K = fma(e1[j], G, G);
+                store2<T, VEC>(p.dx + o, mul(Gm, si), all || a0, all || a1);
+                store2<T, VEC>(p.di + o, mul(mul(Gm, six), mul(ei, si)), all || a0, all || a1);
+                store2<T, VEC>(p.dr + o, mul(mul(dl, mul(A, sr)), mul(er, sr)), all || a0, all || a1);
+            }
+        };
+        if (t.full) walk(true);
+        else walk(false);
+        sm.dA[warp][lane] = dA;
+        __syncwarp();  // this warp's part of the stage is read
+        load(k + NS);
+        A = rates(k + 1);
     }
-    // k tiles are through; the scan warp sums the last two's dA behind two more arrivals
-    for (int j = 0; j < 2; ++j) arrive_warp(&sync.parts[(k + j) & 1], lane);
+    arrive_warp(&sync.parts, lane);  // for the last tile's dA
 }
 
 // Column sums of a [rows, C] array: 32 columns a block, 32 rows at a time, each
@@ -892,14 +945,15 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
     }
 }
 
-// A persistent grid: as many blocks as the GPU holds at once, or one a tile.
+// A persistent grid: one block an SM, or one a tile.
 template <typename K, typename A>
-cudaError_t launch_tiles(K kernel, int smem, int per_sm, const GlrShape &s, A &a, cudaStream_t stream) {
+cudaError_t launch_tiles(K kernel, int smem, const GlrShape &s, A &a, cudaStream_t stream) {
     const int64_t tiles = int64_t(s.nct) * s.nc * (s.nseq ? 1 : s.batch);
-    const int64_t room = int64_t(device_sm_count()) * per_sm;
+    const int64_t room = device_sm_count();
     a.tiles = int(tiles);
+    a.dv = TileDivide{Divide::by(uint32_t(s.nct)), Divide::by(uint32_t(s.batch))};
     if (!smem_attr_once(reinterpret_cast<const void *>(kernel), smem)) return cudaErrorInvalidValue;
-    kernel<<<unsigned(tiles < room ? tiles : room), kThreads, smem, stream>>>(a);
+    kernel<<<unsigned(tiles < room ? tiles : room), kBlock, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -913,7 +967,7 @@ cudaError_t forward_typed(const GlrShape &s, const void *x, const void *r, const
     a.A = A; a.h0 = h0; a.y = static_cast<T *>(y); a.fin = fin; a.states = states;
     a.pk = packed ? *packed : GlrPacked{};
     a.err = err;
-    return launch_tiles(glr_forward_kernel<T, VEC, PACK>, FwdPlan<T>::smem, FwdPlan<T>::kPerSm, s, a, stream);
+    return launch_tiles(glr_forward_kernel<T, VEC, PACK>, FwdPlan<T>::smem, s, a, stream);
 }
 
 template <typename T, bool VEC, bool PACK>
@@ -929,7 +983,7 @@ cudaError_t backward_typed(const GlrShape &s, const void *x, const void *r, cons
     a.A = A; a.states = states; a.dfin = dfin;
     a.dx = static_cast<T *>(dx); a.dr = static_cast<T *>(dr); a.di = static_cast<T *>(di);
     a.dinit = dinit; a.dA_part = dA_part; a.err = err;
-    return launch_tiles(glr_backward_kernel<T, VEC, PACK>, BwdPlan<T, PACK>::smem, BwdPlan<T, PACK>::kPerSm, s, a, stream);
+    return launch_tiles(glr_backward_kernel<T, VEC, PACK>, BwdPlan<T, PACK>::smem, s, a, stream);
 }
 
 // rows of whole 16-byte vectors

@@ -162,14 +162,17 @@ def test_prefill_then_steps_is_one_sequence(oracle):
     close(state, fr)
 
 
-def test_saturated_gates(oracle):
+@pytest.mark.parametrize("seed", range(5))
+def test_saturated_gates(oracle, seed):
     """Gates open and closed as far as they go, decays that vanish, A = 0: finite,
     and the reference's values; a NaN stays in its channel from its token on."""
     B, T, C = 1, 130, 8
     p = problem((B, T, C), "f32", seed=9)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
     vals = torch.tensor([-200.0, -60.0, -30.0, 0.0, 30.0, 60.0, 200.0, 1.0], device=DEV)
-    p["r"] = vals[torch.randint(0, 8, (B, T, C), device=DEV)]
-    p["i"] = vals[torch.randint(0, 8, (B, T, C), device=DEV)]
+    p["r"] = vals[torch.randint(0, 8, (B, T, C), device=DEV, generator=gen)]
+    p["i"] = vals[torch.randint(0, 8, (B, T, C), device=DEV, generator=gen)]
     p["A"] = torch.tensor([0.0, -1e-6, -1e-3, -0.5, -1.0, -8.0, -80.0, -1e4], device=DEV)
     y, saved = binding.glr_forward(p["x"], p["r"], p["i"], p["A"], init_state=p["h0"], save="inputs")
     g = binding.glr_backward(p["dy"], saved)
