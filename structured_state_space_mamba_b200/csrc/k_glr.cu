@@ -311,16 +311,14 @@ __device__ __forceinline__ bool set(float2 v) { return set(v.x) && set(v.y); }
 __device__ __forceinline__ bool set(float4 v) { return set(v.x) && set(v.y) && set(v.z) && set(v.w); }
 
 constexpr int kWindow = 16;  // predecessors that a tile looks back over
-constexpr int kBatch = 8;    // sums fetched at a time
+constexpr int kBatch = 4;    // sums fetched at a time
 
 // The state that enters the tile, for one warp (t.rank > 0): the outgoing state of
 // the nearest predecessor that has published it, taken through the sums of those
-// in between, in their order.  `h` comes in as get_state() of the tile before,
-// fetched ahead.  Otherwise lanes 0 .. 15 watch the predecessors' states, lanes
+// in between, in their order.  Lanes 0 .. 15 watch the predecessors' states, lanes
 // 16 .. 31 their sums.  Gives up with the error word set after kWaitLimitNs.
 __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, int lane, float2 &h,
                                           unsigned int *err) {
-    if (__all_sync(0xffffffffu, set(h))) return true;
     const int window = min(t.rank, kWindow), mine = lane % kWindow;
     const int64_t watched = (t.tile - int64_t(mine + 1) * t.stride) * 32;
     const void *f = lane < kWindow ? static_cast<const void *>(ws.state + watched)
@@ -328,6 +326,8 @@ __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, i
     uint64_t t0 = 0;
     for (uint32_t n = 0;; ++n) {
         const uint32_t v = mine < window ? get_word(f) : kUnset;
+        h = get_state(ws, t.tile - int64_t(t.stride), lane);
+        if (__all_sync(0xffffffffu, set(h))) return true;  // the tile before has published: one trip
         const uint32_t seen = __ballot_sync(0xffffffffu, v != kUnset);
         const uint32_t states = seen & ((1u << kWindow) - 1u), sums = seen >> kWindow;
         if (states) {
@@ -442,10 +442,9 @@ struct Tickets {
 constexpr int kGroups = 3;
 constexpr int kBlock = kGroups * kGroupThreads;
 
-template <int NS>
+// The tiles of a group, in a ring: tile k + NS + 2 is set while k is finished.
+constexpr int kInfos = 8;
 struct Sync {
-    // tile k + NS + 1 is known when tile k is finished
-    static constexpr int kInfos = NS <= 2 ? 4 : 8;
     uint64_t parts, ready;
     Tile tile[kInfos];
 };
@@ -480,7 +479,8 @@ struct FwdPlan {
         Stage stage[kStages][kWarps];
         // products and sums of the warps' tokens; in their place then the states before them
         float4 part[kWarps][32];
-        Sync<kStages> sync;
+        Sync sync;
+        static_assert(kStages + 3 <= kInfos, "a tile's place is taken while it is in use");
     };
     static constexpr int smem = kGroups * sizeof(Smem);
     static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
@@ -495,12 +495,12 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
     const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
     typename Plan::Smem &sm = reinterpret_cast<typename Plan::Smem *>(smem_raw)[group];
-    Sync<NS> &sync = sm.sync;
+    Sync &sync = sm.sync;
     const int C = p.s.C;
     Tickets tickets(p.ws.ticket, p.tiles, kGroups, group);
     auto set_tile = [&](int k, uint32_t raw) {
         const int n = Tickets::tile_of(raw);
-        Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        Tile &t = sync.tile[k & (kInfos - 1)];
         if (n < p.tiles) t = decode_tile(p.s, p.dv, n, false);
         else t.tile = -1;
     };
@@ -508,7 +508,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         tc::mbar_init(&sync.parts, kWarps);
         tc::mbar_init(&sync.ready, 1);
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
@@ -516,7 +516,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         uint32_t next = 0;  // a ticket taken one tile ago
         if (lane == 0) next = tickets.take();
         for (int k = 0;; ++k) {
-            const Tile t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+            const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
             uint32_t later = 0;
             if (lane == 0) later = tickets.take();
@@ -534,14 +534,8 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             }
             if (!t.first) {
                 if (!t.last) put_sums(p.ws, t.tile, lane, P, S);
-                h = get_state(p.ws, t.tile - int64_t(t.stride), lane);
+                look_back(p.ws, t, lane, h, p.err);
             }
-            if (lane == 0) {  // while the state is on its way
-                set_tile(k + NS + 1, next);
-                next = later;
-            }
-            __syncwarp();
-            if (!t.first) look_back(p.ws, t, lane, h, p.err);
             const float2 out = fma(P, h, S);
             if (!t.last) put_state(p.ws, t.tile, lane, out);
             const float2 start = h;
@@ -554,12 +548,17 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             arrive_warp(&sync.ready, lane);
             if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, start, a0, a1);
             if (t.last && p.fin) store2<float, VEC>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
+            if (lane == 0) {
+                set_tile(k + NS + 2, next);
+                next = later;
+            }
+            __syncwarp();
         }
         return;
     }
 
     auto load = [&](int k) {
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        const Tile &t = sync.tile[k & (kInfos - 1)];
         if (t.tile >= 0) {
             typename Plan::Stage &st = sm.stage[k % NS][warp];
             T *const dst[3] = {st.x, st.r, st.i};
@@ -569,14 +568,14 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         copy_commit();
     };
     auto rates = [&](int k) -> float2 {  // A of tile k
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        const Tile &t = sync.tile[k & (kInfos - 1)];
         const int c = t.ct * kGlrCols + 2 * lane;
         return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
     for (int k = 0; k < NS; ++k) load(k);
     float2 A = rates(0);
     for (int k = 0;; ++k) {
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        const Tile &t = sync.tile[k & (kInfos - 1)];
         if (t.tile < 0) break;
         const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
@@ -666,8 +665,9 @@ struct BwdPlan {
         // tokens and K behind them
         float4 part[kWarps][32];
         float2 rpart[kWarps][32];  // reverse sums
-        float2 dA[kWarps][32];
-        Sync<kStages> sync;
+        float2 dA[2][kWarps][32];
+        Sync sync;
+        static_assert(kStages + 3 <= kInfos, "a tile's place is taken while it is in use");
     };
     static constexpr int smem = kGroups * sizeof(Smem);
     static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
@@ -683,13 +683,13 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
     const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
     typename Plan::Smem &sm = reinterpret_cast<typename Plan::Smem *>(smem_raw)[group];
-    Sync<NS> &sync = sm.sync;
+    Sync &sync = sm.sync;
     const int C = p.s.C;
     const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
     Tickets tickets(p.ws.ticket, p.tiles, kGroups, group);
     auto set_tile = [&](int k, uint32_t raw) {
         const int n = Tickets::tile_of(raw);
-        Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        Tile &t = sync.tile[k & (kInfos - 1)];
         if (n < p.tiles) t = decode_tile(p.s, p.dv, n, true);
         else t.tile = -1;
     };
@@ -697,25 +697,25 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         tc::mbar_init(&sync.parts, kWarps);
         tc::mbar_init(&sync.ready, 1);
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
     if (warp == kWarps) {  // the scan warp
         // dA of tile k, which its warps have left by the time they leave the sums of tile k + 1
         auto sum_dA = [&](int k) {
-            const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+            const Tile &t = sync.tile[k & (kInfos - 1)];
             const int c = t.ct * kGlrCols + 2 * lane;
-            float2 sum = sm.dA[0][lane];
+            float2 sum = sm.dA[k & 1][0][lane];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[w][lane]);
+            for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[k & 1][w][lane]);
             store2<float, VEC>(p.dA_part + t.chunk * C + c, sum, c < C, c + 1 < C);
         };
         uint32_t next = 0;  // a ticket taken one tile ago
         if (lane == 0) next = tickets.take();
         int k = 0;
         for (;; ++k) {
-            const Tile t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+            const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
             uint32_t later = 0;
             if (lane == 0) later = tickets.take();
@@ -733,19 +733,10 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             }
             if (!t.last) {
                 if (!t.first) put_sums(p.ws, t.tile, lane, P, R);
-                K = get_state(p.ws, t.tile - int64_t(t.stride), lane);
+                look_back(p.ws, t, lane, K, p.err);
             }
-            if (k >= 1) sum_dA(k - 1);
-            __syncwarp();
-            if (lane == 0) {  // while K is on its way
-                set_tile(k + NS + 1, next);
-                next = later;
-            }
-            __syncwarp();
-            if (!t.last) look_back(p.ws, t, lane, K, p.err);
             const float2 out = fma(P, K, R);
             if (!t.first) put_state(p.ws, t.tile, lane, out);
-            if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
             float2 q[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
@@ -760,6 +751,14 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 K = fma(q[w], K, sm.rpart[w][lane]);
             }
             arrive_warp(&sync.ready, lane);
+            if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
+            if (k >= 1) sum_dA(k - 1);
+            __syncwarp();
+            if (lane == 0) {
+                set_tile(k + NS + 2, next);
+                next = later;
+            }
+            __syncwarp();
         }
         if (k > 0) {  // the last tile: its warps say when they are through
             tc::mbar_wait(&sync.parts, k & 1, p.err);
@@ -769,7 +768,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     }
 
     auto load = [&](int k) {
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        const Tile &t = sync.tile[k & (kInfos - 1)];
         if (t.tile >= 0) {
             typename Plan::Stage &st = sm.stage[k % NS][warp];
             if constexpr (PACK) {
@@ -796,7 +795,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         copy_commit();
     };
     auto rates = [&](int k) -> float2 {  // A of tile k
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        const Tile &t = sync.tile[k & (kInfos - 1)];
         const int c = t.ct * kGlrCols + 2 * lane;
         return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
@@ -804,7 +803,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     float2 A = rates(0);
     int k = 0;
     for (;; ++k) {
-        const Tile &t = sync.tile[k & (Sync<NS>::kInfos - 1)];
+        const Tile &t = sync.tile[k & (kInfos - 1)];
         if (t.tile < 0) break;
         const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;
@@ -887,7 +886,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         };
         if (t.full) walk(true);
         else walk(false);
-        sm.dA[warp][lane] = dA;
+        sm.dA[k & 1][warp][lane] = dA;
         __syncwarp();  // this warp's part of the stage is read
         load(k + NS);
         A = rates(k + 1);
