@@ -523,7 +523,8 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = both(0.f);
-            if (t.first && p.h0) h = load2<VEC>(p.h0 + int64_t(t.row) * C + c, a0, a1);
+            if (!t.first) h = get_state(p.ws, t.tile - int64_t(t.stride), lane);  // it may be there by now
+            else if (p.h0) h = load2<VEC>(p.h0 + int64_t(t.row) * C + c, a0, a1);
             tc::mbar_wait(&sync.parts, k & 1, p.err);
             float2 P = both(1.f), S = both(0.f);
 #pragma unroll
@@ -532,7 +533,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
                 P = mul(P, make_float2(q.x, q.y));
                 S = fma(make_float2(q.x, q.y), S, make_float2(q.z, q.w));
             }
-            if (!t.first) {
+            if (!t.first && !__all_sync(0xffffffffu, set(h))) {
                 if (!t.last) put_sums(p.ws, t.tile, lane, P, S);
                 look_back(p.ws, t, lane, h, p.err);
             }
@@ -722,7 +723,8 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = load2<VEC>(p.states + t.chunk * C + c, a0, a1), K = both(0.f);
-            if (t.last && p.dfin) K = load2<VEC>(p.dfin + int64_t(t.row) * C + c, a0, a1);
+            if (!t.last) K = get_state(p.ws, t.tile - int64_t(t.stride), lane);
+            else if (p.dfin) K = load2<VEC>(p.dfin + int64_t(t.row) * C + c, a0, a1);
             tc::mbar_wait(&sync.parts, k & 1, p.err);
             float2 P = both(1.f), R = both(0.f);
 #pragma unroll
@@ -731,7 +733,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 P = mul(P, q);
                 R = fma(q, R, sm.rpart[w][lane]);
             }
-            if (!t.last) {
+            if (!t.last && !__all_sync(0xffffffffu, set(K))) {
                 if (!t.first) put_sums(p.ws, t.tile, lane, P, R);
                 look_back(p.ws, t, lane, K, p.err);
             }
