@@ -310,48 +310,42 @@ __device__ __forceinline__ bool set(float v) { return __float_as_uint(v) != kUns
 __device__ __forceinline__ bool set(float2 v) { return set(v.x) && set(v.y); }
 __device__ __forceinline__ bool set(float4 v) { return set(v.x) && set(v.y) && set(v.z) && set(v.w); }
 
-constexpr int kWindow = 16;  // predecessors that a tile looks back over
-constexpr int kBatch = 4;    // sums fetched at a time
+constexpr int kWindow = 4;  // predecessors that a tile looks back over
 
 // The state that enters the tile, for one warp (t.rank > 0): the outgoing state of
 // the nearest predecessor that has published it, taken through the sums of those
-// in between, in their order.  Lanes 0 .. 15 watch the predecessors' states, lanes
-// 16 .. 31 their sums.  Gives up with the error word set after kWaitLimitNs.
+// in between, in their order.  Every round fetches all of them, so that a round
+// is one trip through L2, and every lane goes by its own words.  Gives up with
+// the error word set after kWaitLimitNs.
 __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, int lane, float2 &h,
                                           unsigned int *err) {
-    const int window = min(t.rank, kWindow), mine = lane % kWindow;
-    const int64_t watched = (t.tile - int64_t(mine + 1) * t.stride) * 32;
-    const void *f = lane < kWindow ? static_cast<const void *>(ws.state + watched)
-                                   : static_cast<const void *>(ws.sums + watched);
+    const int window = min(t.rank, kWindow);
     uint64_t t0 = 0;
     for (uint32_t n = 0;; ++n) {
-        const uint32_t v = mine < window ? get_word(f) : kUnset;
-        h = get_state(ws, t.tile - int64_t(t.stride), lane);
-        if (__all_sync(0xffffffffu, set(h))) return true;  // the tile before has published: one trip
-        const uint32_t seen = __ballot_sync(0xffffffffu, v != kUnset);
-        const uint32_t states = seen & ((1u << kWindow) - 1u), sums = seen >> kWindow;
-        if (states) {
-            const int d = __ffs(states) - 1;
-            const uint32_t nearer = (1u << d) - 1u;
-            if ((sums & nearer) == nearer) {
-                // one word of each tile has been seen; every lane checks its own
-                h = get_state(ws, t.tile - int64_t(d + 1) * t.stride, lane);
-                bool ok = set(h);
-                for (int e = d; e > 0; e -= kBatch) {
-                    float4 q[kBatch];
+        float2 state[kWindow];
+        float4 sums[kWindow - 1];
 #pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-                        if (k < e) q[k] = get_sums(ws, t.tile - int64_t(e - k) * t.stride, lane);
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k)
-                        if (k < e) {
-                            ok = ok && set(q[k]);
-                            h = fma(make_float2(q[k].x, q[k].y), h, make_float2(q[k].z, q[k].w));
-                        }
-                }
-                if (__all_sync(0xffffffffu, ok)) return true;
+        for (int d = 0; d < kWindow; ++d) {
+            const int64_t tile = t.tile - int64_t(d + 1) * t.stride;
+            state[d] = both(__uint_as_float(kUnset));
+            if (d < window) state[d] = get_state(ws, tile, lane);
+            if (d < kWindow - 1) {
+                sums[d] = make_float4(0.f, 0.f, 0.f, __uint_as_float(kUnset));
+                if (d < window) sums[d] = get_sums(ws, tile, lane);
             }
         }
+        bool ok = false;
+#pragma unroll
+        for (int d = kWindow - 1; d >= 0; --d) {
+            if (set(state[d])) {
+                h = state[d];
+                ok = true;
+            } else if (d < kWindow - 1) {
+                ok = ok && set(sums[d]);
+                h = fma(make_float2(sums[d].x, sums[d].y), h, make_float2(sums[d].z, sums[d].w));
+            }
+        }
+        if (__all_sync(0xffffffffu, ok)) return true;
         if ((n & 15u) == 15u) {
             const uint64_t now = tc::global_ns();
             if (t0 == 0) t0 = now;
