@@ -465,50 +465,56 @@ PACK8_BLOCK = 64  # SSD_PACK8_BLOCK in include/ssd.h
 _CODE = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 
 
-def _same(name, t, like, shape=None, dtype=None):
-    """Refuses a tensor that is not contiguous on `like`'s device with the shape and dtype given (`like`'s)."""
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-    if t.dtype != (dtype or like.dtype):
-        raise ValueError(f"{name} must be {dtype or like.dtype}")
-    if t.shape != (like.shape if shape is None else shape):
-        raise ValueError(f"{name} must be {tuple(like.shape if shape is None else shape)}, is {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _is(t, index, dtype, shape):
+    """Whether t is a contiguous tensor of that dtype and shape on that CUDA device."""
+    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _need(name, t, index, dtype, shape):
+    """Refuses a tensor for which ``_is`` does not hold, with what is wrong."""
+    if _is(t, index, dtype, shape):
+        return
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, is {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _storage(name, x):
-    if not x.is_cuda:
+    """(ssd_dtype_t, CUDA device index) of a tensor in a storage type."""
+    index, code = x.get_device(), _CODE.get(x.dtype)
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    code = _CODE.get(x.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    return code
+    return code, index
 
 
-class _Launch:
-    """The device and stream of one call.  With a stream other than the current
-    one the outputs are allocated for it, so that memory which the current
-    stream still uses is not taken."""
+def _ptr_or_none(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, dev, stream):
-        self.stack = []
-        if torch.cuda.current_device() != dev.index:
-            self.stack.append(torch.cuda.device(dev))
-        current = torch._C._cuda_getCurrentRawStream(dev.index)
-        self.stream = current if stream is None else int(getattr(stream, "cuda_stream", stream))
-        if self.stream != current:
-            self.stack.append(torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=dev)))
 
-    def __enter__(self):
-        for c in self.stack:
-            c.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.stack):
-            c.__exit__(*exc)
-        return False
+def _launch(index, stream, call, *args):
+    """call(stream, *args) with the tensors' device current.  With a stream other
+    than the current one (a torch stream, or its handle) the outputs are
+    allocated for it, so that memory which the current stream still uses is not
+    taken."""
+    if _get_device() != index:
+        with torch.cuda.device(index):
+            return _launch(index, stream, call, *args)
+    current = _raw_stream(index)
+    if stream is not None:
+        handle = int(getattr(stream, "cuda_stream", stream))
+        if handle != current:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=index)):
+                return call(handle, *args)
+    return call(current, *args)
 
 
 class Packed8:
@@ -521,9 +527,9 @@ class Packed8:
         self.codes, self.exps = codes, exps
 
     @classmethod
-    def empty(cls, shape, device):
-        return cls(torch.empty(shape, dtype=torch.int8, device=device),
-                   torch.empty((*shape[:-1], -(-shape[-1] // PACK8_BLOCK)), dtype=torch.uint8, device=device))
+    def empty_like(cls, x):
+        return cls(x.new_empty(x.shape, dtype=torch.int8),
+                   x.new_empty((*x.shape[:-1], -(-x.shape[-1] // PACK8_BLOCK)), dtype=torch.uint8))
 
     @property
     def shape(self):
@@ -532,45 +538,49 @@ class Packed8:
     def _c(self):
         return _Packed8(self.codes.data_ptr(), self.exps.data_ptr())
 
-
-def _check_packed(name, p, like=None, shape=None):
-    if not isinstance(p, Packed8):
-        raise ValueError(f"{name} must be a Packed8")
-    if not p.codes.is_cuda or p.codes.dim() < 1:
-        raise ValueError(f"{name} must hold CUDA tensors")
-    _same(f"{name}.codes", p.codes, p.codes if like is None else like, shape or p.codes.shape, torch.int8)
-    want = (*p.codes.shape[:-1], -(-p.codes.shape[-1] // PACK8_BLOCK))
-    _same(f"{name}.exps", p.exps, p.codes, want, torch.uint8)
+    def _check(self, name, index, shape):
+        _need(f"{name}.codes", self.codes, index, torch.int8, shape)
+        _need(f"{name}.exps", self.exps, index, torch.uint8, (*shape[:-1], -(-shape[-1] // PACK8_BLOCK)))
 
 
 def pack8(x, stream=None):
     """``x`` [..., channels] (float32 or bfloat16) as an 8-bit checkpoint: one
     signed byte a value and one power-of-two step for every 64 values of a row,
     off by at most 1/127.5 of the largest magnitude among them."""
-    code = _storage("x", x)
+    code, index = _storage("x", x)
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError("x must be contiguous with at least one dimension")
+    return _launch(index, stream, _pack8, x, code)
+
+
+def _pack8(st, x, code):
     cols = x.shape[-1]
-    with _Launch(x.device, stream) as st:
-        p = Packed8.empty(x.shape, x.device)
-        c = p._c()
-        _check(load().ssd_pack8(x.numel() // cols if cols else 0, cols, code, x.data_ptr(), ctypes.byref(c), st))
+    p = Packed8.empty_like(x)
+    _check(load().ssd_pack8(x.numel() // cols if cols else 0, cols, code, x.data_ptr(), ctypes.byref(p._c()), st))
     return p
 
 
 def unpack8(packed, dtype=torch.bfloat16, out=None, stream=None):
     """The values of a checkpoint in float32 or bfloat16 (exact in either)."""
-    _check_packed("packed", packed)
-    if out is not None:
-        _same("out", out, packed.codes, packed.shape, dtype)
+    if not isinstance(packed, Packed8):
+        raise ValueError("packed must be a Packed8")
+    index = packed.codes.get_device()
+    if index < 0 or packed.codes.dim() < 1:
+        raise ValueError("packed must hold CUDA tensors of at least one dimension")
+    packed._check("packed", index, packed.shape)
     if dtype not in _CODE:
         raise ValueError("dtype must be float32 or bfloat16")
+    if out is not None:
+        _need("out", out, index, dtype, packed.shape)
+    return _launch(index, stream, _unpack8, packed, dtype, out)
+
+
+def _unpack8(st, packed, dtype, out):
     cols = packed.shape[-1]
-    with _Launch(packed.codes.device, stream) as st:
-        out = torch.empty(packed.shape, dtype=dtype, device=packed.codes.device) if out is None else out
-        c = packed._c()
-        _check(load().ssd_unpack8(packed.codes.numel() // cols if cols else 0, cols, _CODE[dtype], ctypes.byref(c),
-                                  out.data_ptr(), st))
+    if out is None:
+        out = packed.codes.new_empty(packed.shape, dtype=dtype)
+    _check(load().ssd_unpack8(packed.codes.numel() // cols if cols else 0, cols, _CODE[dtype],
+                              ctypes.byref(packed._c()), out.data_ptr(), st))
     return out
 
 
@@ -581,13 +591,6 @@ class GlrSaved:
 
     def __init__(self, x, r, i, A, chunk_states, cu, rows):
         self.x, self.r, self.i, self.A, self.chunk_states, self.cu, self.rows = x, r, i, A, chunk_states, cu, rows
-
-
-def _glr_dims(x):
-    code = _storage("x", x)
-    if x.dim() != 3:
-        raise ValueError("x must be [batch, seqlen, channels]")
-    return GlrDims(x.shape[0], x.shape[1], x.shape[2], code, 0)
 
 
 def glr_forward(x, r, i, A, init_state=None, cu_seqlens=None, return_final_state=False, save=None, out=None,
@@ -602,44 +605,44 @@ def glr_forward(x, r, i, A, init_state=None, cu_seqlens=None, return_final_state
     "inputs" refers to x, r and i themselves, "packed8" writes 8-bit
     checkpoints of them in the same pass.  Returns y plus, as asked, the final
     state and the saved (in that order)."""
-    dims = _glr_dims(x)
-    _same("x", x, x)
-    _same("r", r, x)
-    _same("i", i, x)
-    C = x.shape[2]
-    _same("A", A, x, (C,), torch.float32)
+    code, index = _storage("x", x)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 3:
+        raise ValueError("x must be [batch, seqlen, channels]")
+    for name, t in (("x", x), ("r", r), ("i", i)):
+        _need(name, t, index, dtype, shape)
+    B, T, C = shape
+    _need("A", A, index, torch.float32, (C,))
     if save not in (None, "inputs", "packed8"):
         raise ValueError('save must be None, "inputs" or "packed8"')
     cu = None if cu_seqlens is None else _cu_array(cu_seqlens)
-    nseq = 0 if cu is None else cu.size - 1
-    rows = nseq if cu is not None else x.shape[0]
+    rows = B if cu is None else cu.size - 1
     if init_state is not None:
-        _same("init_state", init_state, x, (rows, C), torch.float32)
+        _need("init_state", init_state, index, torch.float32, (rows, C))
     if out is not None:
-        _same("out", out, x)
-    lib = load()
-    cu_p = None if cu is None else cu.ctypes.data
-    states = packed = final = None
-    with _Launch(x.device, stream) as st:
-        y = torch.empty_like(x) if out is None else out
-        if return_final_state:
-            final = torch.empty((rows, C), dtype=torch.float32, device=x.device)
-        if save is not None:
-            states = torch.empty((lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C), dtype=torch.float32,
-                                 device=x.device)
-            if save == "packed8":
-                packed = [Packed8.empty(x.shape, x.device) for _ in range(3)]
-        pk = None if packed is None else (_Packed8 * 3)(*(p._c() for p in packed))
-        _check(lib.ssd_glr_forward(
-            ctypes.byref(dims), cu_p, nseq, x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
-            None if init_state is None else init_state.data_ptr(), y.data_ptr(),
-            None if final is None else final.data_ptr(), None if states is None else states.data_ptr(), pk, st))
-    res = [y]
-    if return_final_state:
-        res.append(final)
+        _need("out", out, index, dtype, shape)
+    return _launch(index, stream, _glr_forward, GlrDims(B, T, C, code, 0), x, r, i, A, init_state, cu, rows,
+                   return_final_state, save, out)
+
+
+def _glr_forward(st, dims, x, r, i, A, init_state, cu, rows, return_final_state, save, out):
+    lib, C = load(), dims.channels
+    cu_p, nseq = (None, 0) if cu is None else (cu.ctypes.data, rows)
+    y = torch.empty_like(x) if out is None else out
+    final = A.new_empty((rows, C)) if return_final_state else None
+    states = packed = pk = None
     if save is not None:
-        res.append(GlrSaved(*(packed or (x, r, i)), A, states, cu, rows))
-    return res[0] if len(res) == 1 else tuple(res)
+        states = A.new_empty((lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C))
+        if save == "packed8":
+            packed = [Packed8.empty_like(x) for _ in range(3)]
+            pk = (_Packed8 * 3)(*(p._c() for p in packed))
+    _check(lib.ssd_glr_forward(ctypes.byref(dims), cu_p, nseq, x.data_ptr(), r.data_ptr(), i.data_ptr(),
+                               A.data_ptr(), _ptr_or_none(init_state), y.data_ptr(), _ptr_or_none(final),
+                               _ptr_or_none(states), pk, st))
+    if save is None:
+        return (y, final) if return_final_state else y
+    saved = GlrSaved(*(packed or (x, r, i)), A, states, cu, rows)
+    return (y, final, saved) if return_final_state else (y, saved)
 
 
 def glr_backward(dy, saved, dfinal_state=None, return_dinit_state=False, stream=None):
@@ -648,34 +651,41 @@ def glr_backward(dy, saved, dfinal_state=None, return_dinit_state=False, stream=
     dx, dr, di (dy's dtype), dA, and dinit_state (None unless asked for)."""
     if not isinstance(saved, GlrSaved):
         raise ValueError("saved must be what glr_forward returned with save=")
-    dims = _glr_dims(dy)
-    _same("dy", dy, dy)
-    C = dy.shape[2]
+    code, index = _storage("dy", dy)
+    shape, dtype = dy.shape, dy.dtype
+    if len(shape) != 3:
+        raise ValueError("dy must be [batch, seqlen, channels]")
+    _need("dy", dy, index, dtype, shape)
+    B, T, C = shape
     packed = isinstance(saved.x, Packed8)
-    for name, t in (("x", saved.x), ("r", saved.r), ("i", saved.i)):
+    for name, t in (("the saved x", saved.x), ("the saved r", saved.r), ("the saved i", saved.i)):
         if packed:
-            _check_packed(f"the saved {name}", t, dy, dy.shape)
+            t._check(name, index, shape)
         else:
-            _same(f"the saved {name}", t, dy)
-    _same("the saved A", saved.A, dy, (C,), torch.float32)
-    cu = saved.cu
-    nseq = 0 if cu is None else cu.size - 1
-    lib = load()
-    cu_p = None if cu is None else cu.ctypes.data
-    _same("the saved chunk_states", saved.chunk_states, dy,
-          (lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C), torch.float32)
+            _need(name, t, index, dtype, shape)
+    _need("the saved A", saved.A, index, torch.float32, (C,))
     if dfinal_state is not None:
-        _same("dfinal_state", dfinal_state, dy, (saved.rows, C), torch.float32)
-    with _Launch(dy.device, stream) as st:
-        dx, dr, di, dA = (torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(dy),
-                          torch.empty_like(saved.A))
-        dinit = torch.empty((saved.rows, C), dtype=torch.float32, device=dy.device) if return_dinit_state else None
-        pk = (_Packed8 * 3)(saved.x._c(), saved.r._c(), saved.i._c()) if packed else None
-        ins = (None, None, None) if packed else (saved.x.data_ptr(), saved.r.data_ptr(), saved.i.data_ptr())
-        _check(lib.ssd_glr_backward(
-            ctypes.byref(dims), cu_p, nseq, *ins, pk, saved.A.data_ptr(), saved.chunk_states.data_ptr(),
-            dy.data_ptr(), None if dfinal_state is None else dfinal_state.data_ptr(), dx.data_ptr(), dr.data_ptr(),
-            di.data_ptr(), dA.data_ptr(), None if dinit is None else dinit.data_ptr(), st))
+        _need("dfinal_state", dfinal_state, index, torch.float32, (saved.rows, C))
+    return _launch(index, stream, _glr_backward, GlrDims(B, T, C, code, 0), dy, saved, packed, dfinal_state,
+                   return_dinit_state, index)
+
+
+def _glr_backward(st, dims, dy, saved, packed, dfinal_state, return_dinit_state, index):
+    lib, C, cu = load(), dims.channels, saved.cu
+    cu_p, nseq = (None, 0) if cu is None else (cu.ctypes.data, saved.rows)
+    _need("the saved chunk_states", saved.chunk_states, index, torch.float32,
+          (lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C))
+    dx, dr, di = torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(dy)
+    dA = torch.empty_like(saved.A)
+    dinit = saved.A.new_empty((saved.rows, C)) if return_dinit_state else None
+    if packed:
+        x = r = i = None
+        pk = (_Packed8 * 3)(saved.x._c(), saved.r._c(), saved.i._c())
+    else:
+        x, r, i, pk = saved.x.data_ptr(), saved.r.data_ptr(), saved.i.data_ptr(), None
+    _check(lib.ssd_glr_backward(ctypes.byref(dims), cu_p, nseq, x, r, i, pk, saved.A.data_ptr(),
+                                saved.chunk_states.data_ptr(), dy.data_ptr(), _ptr_or_none(dfinal_state),
+                                dx.data_ptr(), dr.data_ptr(), di.data_ptr(), dA.data_ptr(), _ptr_or_none(dinit), st))
     return dict(dx=dx, dr=dr, di=di, dA=dA, dinit_state=dinit)
 
 
@@ -683,45 +693,46 @@ def glr_step(state, x, r, i, A, out=None, stream=None):
     """One token of the gated linear recurrence through ``ssd_glr_step``: ``state``
     [B, C] float32 is updated in place and the output is returned.  x, r, i
     [B, C] (float32 or bfloat16, one dtype); A [C] float32."""
-    code = _storage("x", x)
-    if x.dim() != 2:
+    code, index = _storage("x", x)
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2:
         raise ValueError("x must be [batch, channels]")
-    _same("x", x, x)
-    _same("r", r, x)
-    _same("i", i, x)
-    B, C = x.shape
-    _same("A", A, x, (C,), torch.float32)
-    _same("state", state, x, x.shape, torch.float32)
+    for name, t in (("x", x), ("r", r), ("i", i)):
+        _need(name, t, index, dtype, shape)
+    _need("A", A, index, torch.float32, shape[1:])
+    _need("state", state, index, torch.float32, shape)
     if out is not None:
-        _same("out", out, x)
-    dims = GlrDims(B, 1, C, code, 0)
-    with _Launch(x.device, stream) as st:
-        y = torch.empty_like(x) if out is None else out
-        _check(load().ssd_glr_step(ctypes.byref(dims), x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
-                                   state.data_ptr(), y.data_ptr(), st))
+        _need("out", out, index, dtype, shape)
+    return _launch(index, stream, _glr_step, GlrDims(shape[0], 1, shape[1], code, 0), state, x, r, i, A, out)
+
+
+def _glr_step(st, dims, state, x, r, i, A, out):
+    y = torch.empty_like(x) if out is None else out
+    _check(load().ssd_glr_step(ctypes.byref(dims), x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(),
+                               state.data_ptr(), y.data_ptr(), st))
     return y
 
 
 def _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved):
-    code = _storage("B", B)
-    if B.dim() != 4:
+    code, index = _storage("B", B)
+    shape = B.shape
+    if len(shape) != 4:
         raise ValueError("B and C must be [batch, seqlen, ngroups, dstate]")
-    bsz, T, G, N = B.shape
-    for name, t in (("B", B), ("C", C)):
-        if t.device != B.device or t.dtype != B.dtype or t.shape != B.shape:
-            raise ValueError("B and C must have one shape, dtype and device")
-        s = t.stride()
-        if (N > 1 and s[3] != 1) or (G > 1 and s[2] != N):
-            raise ValueError(f"a token's values of {name} must be contiguous")
-    if positions.dtype != torch.int64:
-        raise ValueError("positions must be int64")
-    _same("positions", positions, B, (bsz, T), torch.int64)
-    _same("inv_freq", inv_freq, B, (inv_freq.numel(),), torch.float32)
-    for name, t in (("weight_B", weight_B), ("weight_C", weight_C)):
-        if t is not None:
-            _same(name, t, B, (N,), torch.float32)
-    (b0, b1), (c0, c1) = B.stride()[:2], C.stride()[:2]
-    return RotateDims(bsz, T, G, N, 2 * inv_freq.numel(), b0, b1, c0, c1, code, 1 if interleaved else 0, float(eps), 0)
+    if C.get_device() != index or C.dtype is not B.dtype or C.shape != shape:
+        raise ValueError("B and C must have one shape, dtype and device")
+    bsz, T, G, N = shape
+    b0, b1, b2, b3 = B.stride()
+    c0, c1, c2, c3 = C.stride()
+    if (N > 1 and (b3 != 1 or c3 != 1)) or (G > 1 and (b2 != N or c2 != N)):
+        raise ValueError("a token's values of B and of C must be contiguous")
+    _need("positions", positions, index, torch.int64, (bsz, T))
+    half = inv_freq.numel()
+    _need("inv_freq", inv_freq, index, torch.float32, (half,))
+    if weight_B is not None:
+        _need("weight_B", weight_B, index, torch.float32, (N,))
+    if weight_C is not None:
+        _need("weight_C", weight_C, index, torch.float32, (N,))
+    return index, RotateDims(bsz, T, G, N, 2 * half, b0, b1, c0, c1, code, 1 if interleaved else 0, eps, 0)
 
 
 def norm_rotate(B, C, positions, inv_freq, weight_B=None, weight_C=None, eps=1e-5, interleaved=False, stream=None):
@@ -733,13 +744,15 @@ def norm_rotate(B, C, positions, inv_freq, weight_B=None, weight_C=None, eps=1e-
     inv_freq [rotary / 2] float32, rotary at most dstate; weights [dstate]
     float32 or None.  Pairs are (j, j + rotary / 2), or neighbours with
     ``interleaved``.  Returns (B, C), contiguous."""
-    dims = _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved)
-    with _Launch(B.device, stream) as st:
-        Bo, Co = (torch.empty(B.shape, dtype=B.dtype, device=B.device) for _ in range(2))
-        _check(load().ssd_norm_rotate(
-            ctypes.byref(dims), B.data_ptr(), C.data_ptr(), positions.data_ptr(),
-            inv_freq.data_ptr() if dims.rotary else None, None if weight_B is None else weight_B.data_ptr(),
-            None if weight_C is None else weight_C.data_ptr(), Bo.data_ptr(), Co.data_ptr(), st))
+    index, dims = _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved)
+    return _launch(index, stream, _norm_rotate, dims, B, C, positions, inv_freq, weight_B, weight_C)
+
+
+def _norm_rotate(st, dims, B, C, positions, inv_freq, weight_B, weight_C):
+    Bo, Co = B.new_empty(B.shape), C.new_empty(C.shape)
+    _check(load().ssd_norm_rotate(ctypes.byref(dims), B.data_ptr(), C.data_ptr(), positions.data_ptr(),
+                                  inv_freq.data_ptr() or None, _ptr_or_none(weight_B), _ptr_or_none(weight_C),
+                                  Bo.data_ptr(), Co.data_ptr(), st))
     return Bo, Co
 
 
@@ -748,19 +761,21 @@ def norm_rotate_backward(dB_out, dC_out, B, C, positions, inv_freq, weight_B=Non
     """Gradients of ``norm_rotate`` through ``ssd_norm_rotate_backward``, from the
     cotangents of its outputs and its inputs: a dict with dB, dC (contiguous),
     dweight_B and dweight_C (None without that weight)."""
-    dims = _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved)
-    _same("dB_out", dB_out, B)
-    _same("dC_out", dC_out, B)
-    with _Launch(B.device, stream) as st:
-        dB, dC = torch.empty_like(dB_out), torch.empty_like(dC_out)
-        dwB = None if weight_B is None else torch.empty_like(weight_B)
-        dwC = None if weight_C is None else torch.empty_like(weight_C)
-        _check(load().ssd_norm_rotate_backward(
-            ctypes.byref(dims), dB_out.data_ptr(), dC_out.data_ptr(), B.data_ptr(), C.data_ptr(),
-            positions.data_ptr(), inv_freq.data_ptr() if dims.rotary else None,
-            None if weight_B is None else weight_B.data_ptr(), None if weight_C is None else weight_C.data_ptr(),
-            dB.data_ptr(), dC.data_ptr(), None if dwB is None else dwB.data_ptr(),
-            None if dwC is None else dwC.data_ptr(), st))
+    index, dims = _rotate_dims(B, C, positions, inv_freq, weight_B, weight_C, eps, interleaved)
+    _need("dB_out", dB_out, index, B.dtype, B.shape)
+    _need("dC_out", dC_out, index, B.dtype, B.shape)
+    return _launch(index, stream, _norm_rotate_backward, dims, dB_out, dC_out, B, C, positions, inv_freq, weight_B,
+                   weight_C)
+
+
+def _norm_rotate_backward(st, dims, dB_out, dC_out, B, C, positions, inv_freq, weight_B, weight_C):
+    dB, dC = torch.empty_like(dB_out), torch.empty_like(dC_out)
+    dwB = None if weight_B is None else torch.empty_like(weight_B)
+    dwC = None if weight_C is None else torch.empty_like(weight_C)
+    _check(load().ssd_norm_rotate_backward(
+        ctypes.byref(dims), dB_out.data_ptr(), dC_out.data_ptr(), B.data_ptr(), C.data_ptr(), positions.data_ptr(),
+        inv_freq.data_ptr() or None, _ptr_or_none(weight_B), _ptr_or_none(weight_C), dB.data_ptr(), dC.data_ptr(),
+        _ptr_or_none(dwB), _ptr_or_none(dwC), st))
     return dict(dB=dB, dC=dC, dweight_B=dwB, dweight_C=dwC)
 
 

@@ -50,6 +50,13 @@ cudaError_t launch_glr_backward(const GlrShape &s, bool bf16, const void *x, con
                                 const GlrPacked *packed, const float *A, const float *states, const void *dy,
                                 const float *dfin, void *dx, void *dr, void *di, float *dinit, float *dA_part,
                                 const GlrScratch &ws, unsigned int *err, cudaStream_t stream);
+// rows id[0 .. n) of `to` [., C] from those of `from`, or zeros without it
+constexpr int kGlrRows = 512;
+struct GlrRows {
+    int n;
+    int id[kGlrRows];
+};
+cudaError_t launch_copy_rows(const GlrRows &rows, int C, const float *from, float *to, cudaStream_t stream);
 // dA[c] = sum of the rows of part [rows, C], in a fixed order
 cudaError_t launch_row_sum(const float *part, int64_t rows, int C, float *out, cudaStream_t stream);
 cudaError_t launch_glr_step(int batch, int C, bool bf16, const void *x, const void *r, const void *i,

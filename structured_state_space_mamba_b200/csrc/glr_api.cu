@@ -112,12 +112,14 @@ struct ScratchPlan {
 // An empty sequence leaves its state as it came.
 ssd_status_t copy_empty(const int64_t *cu, int64_t nseq, int64_t C, const float *from, float *to, cudaStream_t st) {
     if (!cu || !to) return SSD_OK;
-    for (int64_t j = 0; j < nseq; ++j) {
-        if (cu[j + 1] != cu[j]) continue;
-        const cudaError_t e =
-            from ? cudaMemcpyAsync(to + j * C, from + j * C, C * sizeof(float), cudaMemcpyDeviceToDevice, st)
-                 : cudaMemsetAsync(to + j * C, 0, C * sizeof(float), st);
-        if (e != cudaSuccess) return SSD_ERR_CUDA;
+    ssd::GlrRows rows;
+    rows.n = 0;
+    for (int64_t j = 0; j <= nseq; ++j) {
+        if (j < nseq && cu[j + 1] == cu[j]) rows.id[rows.n++] = int(j);
+        if (rows.n == ssd::kGlrRows || (j == nseq && rows.n > 0)) {
+            if (ssd::launch_copy_rows(rows, int(C), from, to, st) != cudaSuccess) return SSD_ERR_CUDA;
+            rows.n = 0;
+        }
     }
     return SSD_OK;
 }

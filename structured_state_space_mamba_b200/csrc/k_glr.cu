@@ -908,6 +908,15 @@ row_sum_kernel(const float *__restrict__ part, int64_t rows, int C, float *__res
     }
 }
 
+// the states of empty sequences
+__global__ void __launch_bounds__(256)
+copy_rows_kernel(const __grid_constant__ GlrRows rows, int C, const float *from, float *to) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= C) return;
+    const int64_t o = int64_t(rows.id[blockIdx.y]) * C + c;
+    to[o] = from ? from[o] : 0.f;
+}
+
 // ---------------------------------------------------------------------------
 // decode step
 // ---------------------------------------------------------------------------
@@ -1015,6 +1024,11 @@ cudaError_t launch_glr_backward(const GlrShape &s, bool bf16, const void *x, con
         return backward_typed<decltype(t), decltype(even)::value, decltype(pack)::value>(
             s, x, r, i, packed, A, states, dy, dfin, dx, dr, di, dinit, dA_part, ws, err, stream);
     });
+}
+
+cudaError_t launch_copy_rows(const GlrRows &rows, int C, const float *from, float *to, cudaStream_t stream) {
+    copy_rows_kernel<<<dim3(unsigned((C + 255) / 256), unsigned(rows.n)), 256, 0, stream>>>(rows, C, from, to);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_row_sum(const float *part, int64_t rows, int C, float *out, cudaStream_t stream) {
