@@ -155,7 +155,7 @@ ssd_status_t rotate_shape(const ssd_rotate_dims_t *dims, ssd::RotateShape *s) {
     s->B_batch = a.B_batch_stride; s->B_token = a.B_token_stride;
     s->C_batch = a.C_batch_stride; s->C_token = a.C_token_stride;
     s->T = int(a.seqlen); s->G = int(a.ngroups); s->N = int(a.dstate); s->rotary = int(a.rotary);
-    s->lanes = 1;
+    s->lanes = 4;
     while (s->lanes * 8 < s->N) s->lanes *= 2;
     s->interleaved = a.interleaved ? 1 : 0;
     s->eps = a.eps;

@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "norm_rotate.h"
+#include "tma_host.h"
 
 namespace ssd {
 
@@ -25,24 +26,38 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+// blocks an SM holds, by the registers that they take without spilling
+template <typename T> constexpr int kForwardPerSm = sizeof(T) == 2 ? 6 : 5;
+constexpr int kBackwardPerSm = 4;
 
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+// four values as they lie in memory, and as numbers
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> { using type = uint2; };
+template <> struct Raw<float> { using type = float4; };
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::type fetch4(const T *p) {
+    return __ldg(reinterpret_cast<const typename Raw<T>::type *>(p));
 }
-__device__ __forceinline__ void load4(const float *p, float *v) {
-    const float4 u = __ldg(reinterpret_cast<const float4 *>(p));
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+// two pairs of neighbours, for the packed fp32 operations
+__device__ __forceinline__ void widen4(uint2 u, float2 *v) {
+    v[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    v[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+__device__ __forceinline__ void widen4(float4 u, float2 *v) {
+    v[0] = make_float2(u.x, u.y);
+    v[1] = make_float2(u.z, u.w);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float2 *v) {
+    const __nv_bfloat162 a = __float22bfloat162_rn(v[0]), b = __float22bfloat162_rn(v[1]);
     *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
                                                *reinterpret_cast<const uint32_t *>(&b));
 }
-__device__ __forceinline__ void store4(float *p, const float *v) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void store4(float *p, const float2 *v) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // Sine and cosine of a fraction of a turn in [-1/2, 1/2].  For bf16 storage the
 // hardware functions do: their absolute error (2^-20) is far below a bf16 step
@@ -64,17 +79,21 @@ __device__ __forceinline__ float turn_fraction(double pos, double turns) {
 }
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-// A lane's eight values: where its two vectors of four lie, and how they pair.
+// A lane's eight values, v[0 .. 3] in pairs of neighbours: where its two vectors of
+// four lie, and how they turn.
 //   half-split: the first at 4q of the pairs' first halves, the second rotary/2
-//   further; behind the rotary values, two vectors in a row.
-//   interleaved: two vectors in a row; pairs are neighbours.
+//   further, so that v[0] turns with v[2] and v[1] with v[3]; behind the rotary
+//   values, two vectors in a row.
+//   interleaved: two vectors in a row; each of v turns in itself.
 struct Lane {
     int o0, o1;
+    int pairs;  // how many of the lane's four turn (at most 0: none)
     bool active;
 };
 __device__ __forceinline__ Lane lane_of(const RotateShape &s, int q) {
     Lane l;
     l.active = q * 8 < s.N;
+    l.pairs = s.rotary / 2 - 4 * q;
     if (s.interleaved || q * 8 >= s.rotary) {
         l.o0 = q * 8;
         l.o1 = q * 8 + 4;
@@ -84,180 +103,230 @@ __device__ __forceinline__ Lane lane_of(const RotateShape &s, int q) {
     }
     return l;
 }
-// pair k of a lane: values a(k) and b(k) of its eight
-template <bool INTER>
-__device__ __forceinline__ constexpr int pa(int k) { return INTER ? 2 * k : k; }
-template <bool INTER>
-__device__ __forceinline__ constexpr int pb(int k) { return INTER ? 2 * k + 1 : k + 4; }
 
-// Turns a position by frequency of a lane's four pairs, 4q + k in either order
-// (0 behind the rotary values, which turned() leaves alone).
+// Turns a position by frequency of a lane's four pairs, 4q + k in either order.
 __device__ __forceinline__ void lane_turns(const RotateShape &s, const float *inv_freq, int q, double (&turns)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         turns[k] = 4 * q + k < s.rotary / 2 ? double(__ldg(inv_freq + 4 * q + k)) * kInvTwoPi : 0.0;
 }
-// The lane's pairs rotated by sign times their angles; `pairs` of the four are.
-template <bool INTER>
-__device__ __forceinline__ void turn(float (&v)[8], const float (&sn)[4], const float (&cs)[4], int pairs,
-                                     float sign) {
+// Sines and cosines of a lane's pairs at a position: half-split, (0, 1) and (2, 3) as
+// they meet the values; interleaved, pair by pair.
+template <typename T, bool INTER>
+struct Turn {
+    float2 cs[INTER ? 4 : 2], sn[INTER ? 4 : 2];
+    __device__ __forceinline__ void at(double pos, const double (&turns)[4]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float a = v[pa<INTER>(k)], b = v[pb<INTER>(k)], s = sign * sn[k];
-        if (k < pairs) {
-            v[pa<INTER>(k)] = a * cs[k] - b * s;
-            v[pb<INTER>(k)] = a * s + b * cs[k];
+        for (int k = 0; k < 4; ++k) {
+            float s, c;
+            sincos_turn<T>(turn_fraction(pos, turns[k]), s, c);
+            if (INTER) {
+                cs[k] = both(c);
+                sn[k] = make_float2(-s, s);
+            } else {
+                (k & 1 ? cs[k / 2].y : cs[k / 2].x) = c;
+                (k & 1 ? sn[k / 2].y : sn[k / 2].x) = s;
+            }
         }
     }
+    // turns the values, or back
+    __device__ __forceinline__ void operator()(float2 (&v)[4], int pairs, bool back) const {
+        if (INTER) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < pairs) {
+                    const float2 s = back ? make_float2(-sn[k].x, -sn[k].y) : sn[k];
+                    v[k] = fma(make_float2(v[k].y, v[k].x), s, mul(v[k], cs[k]));
+                }
+        } else if (pairs > 0) {  // all four, as rotary / 2 is a multiple of four
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 a = v[k], b = v[k + 2];
+                const float2 s = back ? make_float2(-sn[k].x, -sn[k].y) : sn[k], m = make_float2(-s.x, -s.y);
+                v[k] = fma(b, m, mul(a, cs[k]));
+                v[k + 2] = fma(a, s, mul(b, cs[k]));
+            }
+        }
+    }
+};
+
+// sums of a and b over LANES neighbouring lanes
+template <int LANES>
+__device__ __forceinline__ void lanes_sum2(float &a, float &b) {
+#pragma unroll
+    for (int o = LANES >> 1; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+}
+__device__ __forceinline__ float square_sum(const float2 (&v)[4]) {
+    float2 s = mul(v[0], v[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s = fma(v[e], v[e], s);
+    return s.x + s.y;
+}
+// a lane's weights, ones without any
+__device__ __forceinline__ void lane_weights(const float *w, const Lane &l, float2 (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int o = e < 2 ? l.o0 + 2 * e : l.o1 + 2 * e - 4;
+        v[e] = l.active && w ? make_float2(__ldg(w + o), __ldg(w + o + 1)) : both(1.f);
+    }
+}
+// where a token's row begins
+__device__ __forceinline__ void token_place(const RotateShape &s, int64_t tok, int64_t &ob, int64_t &oc) {
+    const int64_t row = s.T == s.tokens ? 0 : tok / s.T, t = tok - row * s.T;
+    ob = row * s.B_batch + t * s.B_token;
+    oc = row * s.C_batch + t * s.C_token;
 }
 
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool INTER, int LANES>
+__global__ void __launch_bounds__(kThreads, kForwardPerSm<T>)
 norm_rotate_kernel(const __grid_constant__ RotateShape s, const T *__restrict__ Bm, const T *__restrict__ Cm,
                    const int64_t *__restrict__ positions, const float *__restrict__ inv_freq,
                    const float *__restrict__ wB, const float *__restrict__ wC, T *__restrict__ Bo,
                    T *__restrict__ Co) {
-    const int q = threadIdx.x % s.lanes;
+    constexpr int kPer = kThreads / LANES;  // tokens of a block at a time
+    const int q = threadIdx.x % LANES;
     const Lane l = lane_of(s, q);
     double turns[4];
     lane_turns(s, inv_freq, q, turns);
-    const int pairs = s.rotary / 2 - 4 * q;
-    float wb[8], wc[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int o = e < 4 ? l.o0 + e : l.o1 + e - 4;
-        wb[e] = l.active && wB ? __ldg(wB + o) : 1.f;
-        wc[e] = l.active && wC ? __ldg(wC + o) : 1.f;
-    }
+    float2 wb[4], wc[4];
+    lane_weights(wB, l, wb);
+    lane_weights(wC, l, wc);
     const float inv_n = 1.f / float(s.N);
-    const int per = kThreads / s.lanes;  // tokens of a block at a time
     // whole warps stay in the loop: the sums cross their lanes
-    for (int64_t base = int64_t(blockIdx.x) * per; base < s.tokens; base += int64_t(gridDim.x) * per) {
-        const int64_t tok = base + threadIdx.x / s.lanes;
+    for (int64_t base = int64_t(blockIdx.x) * kPer; base < s.tokens; base += int64_t(gridDim.x) * kPer) {
+        const int64_t tok = base + threadIdx.x / LANES;
         const bool act = l.active && tok < s.tokens;
-        const int64_t row = act ? tok / s.T : 0, t = act ? tok - row * s.T : 0;
-        const T *xb = Bm + row * s.B_batch + t * s.B_token, *xc = Cm + row * s.C_batch + t * s.C_token;
-        const double pos = act ? double(__ldg(positions + tok)) : 0.0;
-        float sn[4], cs[4];
+        int64_t ob = 0, oc = 0;
+        if (act) token_place(s, tok, ob, oc);
+        const T *xb = Bm + ob + int64_t(blockIdx.y) * s.N, *xc = Cm + oc + int64_t(blockIdx.y) * s.N;
+        const int step = int(gridDim.y) * s.N;
+        // the next group's four vectors are on their way while this one's are worked on
+        typename Raw<T>::type next[4] = {};
+        auto fetch = [&](bool more) {
+            if (!act || !more) return;
+            next[0] = fetch4(xb + l.o0);
+            next[1] = fetch4(xb + l.o1);
+            next[2] = fetch4(xc + l.o0);
+            next[3] = fetch4(xc + l.o1);
+            xb += step;
+            xc += step;
+        };
+        fetch(int(blockIdx.y) < s.G);
+        Turn<T, INTER> turn;
+        turn.at(act ? double(__ldg(positions + tok)) : 0.0, turns);
+        int64_t o = (tok * s.G + blockIdx.y) * s.N;
+        for (int g = blockIdx.y; g < s.G; g += gridDim.y, o += step) {
+            float2 b[4], c[4];
+            widen4(next[0], b);
+            widen4(next[1], b + 2);
+            widen4(next[2], c);
+            widen4(next[3], c + 2);
+            fetch(g + int(gridDim.y) < s.G);
+            float sb = square_sum(b), sc = square_sum(c);
+            lanes_sum2<LANES>(sb, sc);
+            sb = rsqrtf(fmaf(sb, inv_n, s.eps));
+            sc = rsqrtf(fmaf(sc, inv_n, s.eps));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sincos_turn<T>(turn_fraction(pos, turns[k]), sn[k], cs[k]);
-        for (int g = blockIdx.y; g < s.G; g += gridDim.y) {
-            float b[8], c[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = c[e] = 0.f;
-            const int64_t gi = int64_t(g) * s.N;
-            if (act) {
-                load4(xb + gi + l.o0, b);
-                load4(xb + gi + l.o1, b + 4);
-                load4(xc + gi + l.o0, c);
-                load4(xc + gi + l.o1, c + 4);
+            for (int e = 0; e < 4; ++e) {
+                b[e] = mul(mul(b[e], both(sb)), wb[e]);
+                c[e] = mul(mul(c[e], both(sc)), wc[e]);
             }
-            float sb = 0.f, sc = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sb = fmaf(b[e], b[e], sb);
-                sc = fmaf(c[e], c[e], sc);
-            }
-            sb = rsqrtf(lanes_sum(sb, s.lanes) * inv_n + s.eps);
-            sc = rsqrtf(lanes_sum(sc, s.lanes) * inv_n + s.eps);
+            turn(b, l.pairs, false);
+            turn(c, l.pairs, false);
             if (!act) continue;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                b[e] *= sb * wb[e];
-                c[e] *= sc * wc[e];
-            }
-            turn<INTER>(b, sn, cs, pairs, 1.f);
-            turn<INTER>(c, sn, cs, pairs, 1.f);
-            const int64_t o = (tok * s.G + g) * s.N;
             store4(Bo + o + l.o0, b);
-            store4(Bo + o + l.o1, b + 4);
+            store4(Bo + o + l.o1, b + 2);
             store4(Co + o + l.o0, c);
-            store4(Co + o + l.o1, c + 4);
+            store4(Co + o + l.o1, c + 2);
         }
     }
 }
 
-// dv of one row from its values x and the cotangent d (rotated back in place);
-// adds the row's share to the weight's gradient.
-template <bool INTER>
-__device__ __forceinline__ void row_backward(const RotateShape &s, float inv_n, const float (&x)[8], float (&d)[8],
-                                             const float (&w)[8], const float (&sn)[4], const float (&cs)[4],
-                                             int pairs, float (&dw)[8]) {
-    turn<INTER>(d, sn, cs, pairs, -1.f);
-    float ss = 0.f, dot = 0.f;
+// dv of one row from its values x, in place of the cotangent d (which is turned
+// back first); adds the row's share to the weight's gradient.
+template <int LANES, typename TURN>
+__device__ __forceinline__ void row_backward(const RotateShape &s, const Lane &l, float inv_n, const TURN &turn,
+                                             const float2 (&x)[4], float2 (&d)[4], const float2 (&w)[4],
+                                             float2 (&dw)[4]) {
+    turn(d, l.pairs, true);
+    float2 z[4], t = both(0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        ss = fmaf(x[e], x[e], ss);
-        dot = fmaf(d[e] * w[e], x[e], dot);
+    for (int e = 0; e < 4; ++e) {
+        z[e] = mul(d[e], w[e]);
+        t = fma(z[e], x[e], t);
     }
-    const float rstd = rsqrtf(lanes_sum(ss, s.lanes) * inv_n + s.eps);
-    const float k = lanes_sum(dot, s.lanes) * inv_n * rstd * rstd;
+    float ss = square_sum(x), dot = t.x + t.y;
+    lanes_sum2<LANES>(ss, dot);
+    const float rstd = rsqrtf(fmaf(ss, inv_n, s.eps)), k = -dot * inv_n * rstd * rstd;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        dw[e] = fmaf(d[e], x[e] * rstd, dw[e]);
-        d[e] = rstd * (d[e] * w[e] - x[e] * k);
+    for (int e = 0; e < 4; ++e) {
+        dw[e] = fma(d[e], mul(x[e], both(rstd)), dw[e]);
+        d[e] = mul(fma(x[e], both(k), z[e]), both(rstd));
     }
 }
 
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool INTER, int LANES>
+__global__ void __launch_bounds__(kThreads, kBackwardPerSm)
 norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__restrict__ dBo,
                             const T *__restrict__ dCo, const T *__restrict__ Bm, const T *__restrict__ Cm,
                             const int64_t *__restrict__ positions, const float *__restrict__ inv_freq,
                             const float *__restrict__ wB, const float *__restrict__ wC, T *__restrict__ dB,
                             T *__restrict__ dC, float *__restrict__ part) {
+    constexpr int kPer = kThreads / LANES;
     __shared__ float red[kWarps][2][256];
-    const int q = threadIdx.x % s.lanes;
+    const int q = threadIdx.x % LANES;
     const Lane l = lane_of(s, q);
     double turns[4];
     lane_turns(s, inv_freq, q, turns);
-    const int pairs = s.rotary / 2 - 4 * q;
-    float wb[8], wc[8], gb[8], gc[8];
+    float2 wb[4], wc[4], gb[4], gc[4];
+    lane_weights(wB, l, wb);
+    lane_weights(wC, l, wc);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int o = e < 4 ? l.o0 + e : l.o1 + e - 4;
-        wb[e] = l.active && wB ? __ldg(wB + o) : 1.f;
-        wc[e] = l.active && wC ? __ldg(wC + o) : 1.f;
-        gb[e] = gc[e] = 0.f;
-    }
+    for (int e = 0; e < 4; ++e) gb[e] = gc[e] = both(0.f);
     const float inv_n = 1.f / float(s.N);
-    const int per = kThreads / s.lanes;
-    for (int64_t base = int64_t(blockIdx.x) * per; base < s.tokens; base += int64_t(gridDim.x) * per) {
-        const int64_t tok = base + threadIdx.x / s.lanes;
+    for (int64_t base = int64_t(blockIdx.x) * kPer; base < s.tokens; base += int64_t(gridDim.x) * kPer) {
+        const int64_t tok = base + threadIdx.x / LANES;
         const bool act = l.active && tok < s.tokens;
-        const int64_t row = act ? tok / s.T : 0, t = act ? tok - row * s.T : 0;
-        const T *xb = Bm + row * s.B_batch + t * s.B_token, *xc = Cm + row * s.C_batch + t * s.C_token;
-        const double pos = act ? double(__ldg(positions + tok)) : 0.0;
-        float sn[4], cs[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sincos_turn<T>(turn_fraction(pos, turns[k]), sn[k], cs[k]);
-        for (int g = 0; g < s.G; ++g) {
-            float b[8], c[8], db[8], dc[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = c[e] = db[e] = dc[e] = 0.f;
-            const int64_t gi = int64_t(g) * s.N, o = (tok * s.G + g) * s.N;
+        int64_t ob = 0, oc = 0;
+        if (act) token_place(s, tok, ob, oc);
+        const T *xb = Bm + ob, *xc = Cm + oc;
+        Turn<T, INTER> turn;
+        turn.at(act ? double(__ldg(positions + tok)) : 0.0, turns);
+        int64_t o = tok * s.G * s.N;
+        for (int g = 0; g < s.G; ++g, o += s.N, xb += s.N, xc += s.N) {
+            typename Raw<T>::type raw[8] = {};
             if (act) {
-                load4(xb + gi + l.o0, b);
-                load4(xb + gi + l.o1, b + 4);
-                load4(dBo + o + l.o0, db);
-                load4(dBo + o + l.o1, db + 4);
-                load4(xc + gi + l.o0, c);
-                load4(xc + gi + l.o1, c + 4);
-                load4(dCo + o + l.o0, dc);
-                load4(dCo + o + l.o1, dc + 4);
+                raw[0] = fetch4(xb + l.o0);
+                raw[1] = fetch4(xb + l.o1);
+                raw[2] = fetch4(dBo + o + l.o0);
+                raw[3] = fetch4(dBo + o + l.o1);
+                raw[4] = fetch4(xc + l.o0);
+                raw[5] = fetch4(xc + l.o1);
+                raw[6] = fetch4(dCo + o + l.o0);
+                raw[7] = fetch4(dCo + o + l.o1);
             }
-            row_backward<INTER>(s, inv_n, b, db, wb, sn, cs, pairs, gb);
-            row_backward<INTER>(s, inv_n, c, dc, wc, sn, cs, pairs, gc);
-            if (!act) continue;
-            store4(dB + o + l.o0, db);
-            store4(dB + o + l.o1, db + 4);
-            store4(dC + o + l.o0, dc);
-            store4(dC + o + l.o1, dc + 4);
+            float2 x[4], d[4];
+            widen4(raw[0], x);
+            widen4(raw[1], x + 2);
+            widen4(raw[2], d);
+            widen4(raw[3], d + 2);
+            row_backward<LANES>(s, l, inv_n, turn, x, d, wb, gb);
+            if (act) {
+                store4(dB + o + l.o0, d);
+                store4(dB + o + l.o1, d + 2);
+            }
+            widen4(raw[4], x);
+            widen4(raw[5], x + 2);
+            widen4(raw[6], d);
+            widen4(raw[7], d + 2);
+            row_backward<LANES>(s, l, inv_n, turn, x, d, wc, gc);
+            if (act) {
+                store4(dC + o + l.o0, d);
+                store4(dC + o + l.o1, d + 2);
+            }
         }
     }
     if (!part) return;
@@ -265,14 +334,16 @@ norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__re
     const int warp = threadIdx.x >> 5;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        for (int o = s.lanes; o < 32; o <<= 1) {
-            gb[e] += __shfl_xor_sync(0xffffffffu, gb[e], o);
-            gc[e] += __shfl_xor_sync(0xffffffffu, gc[e], o);
+        float b = e & 1 ? gb[e / 2].y : gb[e / 2].x, c = e & 1 ? gc[e / 2].y : gc[e / 2].x;
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1) {
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+            c += __shfl_xor_sync(0xffffffffu, c, o);
         }
-        if (l.active && (threadIdx.x & 31) < s.lanes) {
+        if (l.active && (threadIdx.x & 31) < LANES) {
             const int o = e < 4 ? l.o0 + e : l.o1 + e - 4;
-            red[warp][0][o] = gb[e];
-            red[warp][1][o] = gc[e];
+            red[warp][0][o] = b;
+            red[warp][1][o] = c;
         }
     }
     __syncthreads();
@@ -289,6 +360,11 @@ norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__re
 // Pair j is on lane j % 32 (at most four a lane), and so are the values behind
 // the rotary ones.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 struct Row {
     int64_t tok;
     int g;
@@ -330,7 +406,7 @@ norm_rotate_any_kernel(const __grid_constant__ RotateShape s, const T *__restric
             const float v = to_f32<T>(x[n]);
             ss = fmaf(v, v, ss);
         }
-        const float rstd = rsqrtf(lanes_sum(ss, 32) / float(s.N) + s.eps);
+        const float rstd = rsqrtf(warp_sum(ss) / float(s.N) + s.eps);
         const double pos = double(__ldg(positions + w.tok));
         for (int j = lane; j < s.rotary / 2; j += 32) {
             int p, q;
@@ -393,8 +469,8 @@ norm_rotate_backward_any_kernel(const __grid_constant__ RotateShape s, const T *
             ss = fmaf(v, v, ss);
             dot = fmaf(to_f32<T>(d[n]) * (wt ? __ldg(wt + n) : 1.f), v, dot);
         }
-        const float rstd = rsqrtf(lanes_sum(ss, 32) / float(s.N) + s.eps);
-        const float m = lanes_sum(dot, 32) / float(s.N) * rstd * rstd;
+        const float rstd = rsqrtf(warp_sum(ss) / float(s.N) + s.eps);
+        const float m = warp_sum(dot) / float(s.N) * rstd * rstd;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int j = lane + 32 * k;
@@ -452,26 +528,46 @@ bool vectors(const RotateShape &s, bool bf16, const void *Bm, const void *Cm) {
            (reinterpret_cast<uintptr_t>(Cm) & mask) == 0;
 }
 
-constexpr int64_t kMostBlocks = 148 * 16;  // 16 blocks of 128 threads fill an SM
+// Calls f with the order of the pairs and the lanes of a token as types.
+template <typename F>
+void by_lanes(const RotateShape &s, F &&f) {
+    auto with = [&](auto inter) {
+        switch (s.lanes) {
+            case 4: return f(inter, std::integral_constant<int, 4>{});
+            case 8: return f(inter, std::integral_constant<int, 8>{});
+            case 16: return f(inter, std::integral_constant<int, 16>{});
+            default: return f(inter, std::integral_constant<int, 32>{});
+        }
+    };
+    if (s.interleaved) with(std::true_type{});
+    else with(std::false_type{});
+}
+
+// Blocks for `need` portions of work: what the GPU holds at once, every block with
+// as many portions as the next (or one fewer).
+int64_t even_blocks(int64_t need, int per_sm) {
+    const int64_t room = int64_t(device_sm_count()) * per_sm, rounds = (need + room - 1) / room;
+    return (need + rounds - 1) / rounds;
+}
 
 template <typename T>
 cudaError_t forward_typed(const RotateShape &s, const T *Bm, const T *Cm, const int64_t *positions,
                           const float *inv_freq, const float *wB, const float *wC, T *Bo, T *Co, cudaStream_t st) {
     if (vectors(s, sizeof(T) == 2, Bm, Cm)) {
         const int64_t per = kThreads / s.lanes, need = (s.tokens + per - 1) / per;
-        const unsigned gx = unsigned(need < kMostBlocks ? need : kMostBlocks);
+        const unsigned gx = unsigned(even_blocks(need, kForwardPerSm<T>));
         // few tokens (a decode step): the groups go to blocks of their own,
         // as long as the GPU has room
-        int64_t gy = kMostBlocks / gx;
+        int64_t gy = int64_t(device_sm_count()) * kForwardPerSm<T> / gx;
         if (gy > s.G) gy = s.G;
         const dim3 grid(gx, unsigned(gy < 1 ? 1 : gy));
-        if (s.interleaved)
-            norm_rotate_kernel<T, true><<<grid, kThreads, 0, st>>>(s, Bm, Cm, positions, inv_freq, wB, wC, Bo, Co);
-        else
-            norm_rotate_kernel<T, false><<<grid, kThreads, 0, st>>>(s, Bm, Cm, positions, inv_freq, wB, wC, Bo, Co);
+        by_lanes(s, [&](auto inter, auto lanes) {
+            norm_rotate_kernel<T, decltype(inter)::value, decltype(lanes)::value>
+                <<<grid, kThreads, 0, st>>>(s, Bm, Cm, positions, inv_freq, wB, wC, Bo, Co);
+        });
     } else {
         const int64_t need = (s.tokens * s.G * 2 + kWarps - 1) / kWarps;
-        norm_rotate_any_kernel<T><<<unsigned(need < 4 * kMostBlocks ? need : 4 * kMostBlocks), kThreads, 0, st>>>(
+        norm_rotate_any_kernel<T><<<unsigned(even_blocks(need, 16)), kThreads, 0, st>>>(
             s, Bm, Cm, positions, inv_freq, wB, wC, Bo, Co);
     }
     return cudaGetLastError();
@@ -482,12 +578,10 @@ cudaError_t backward_typed(const RotateShape &s, int blocks, const T *dBo, const
                            const int64_t *positions, const float *inv_freq, const float *wB, const float *wC,
                            T *dB, T *dC, float *part, float *dwB, float *dwC, cudaStream_t st) {
     if (vectors(s, sizeof(T) == 2, Bm, Cm)) {
-        if (s.interleaved)
-            norm_rotate_backward_kernel<T, true><<<blocks, kThreads, 0, st>>>(s, dBo, dCo, Bm, Cm, positions,
-                                                                              inv_freq, wB, wC, dB, dC, part);
-        else
-            norm_rotate_backward_kernel<T, false><<<blocks, kThreads, 0, st>>>(s, dBo, dCo, Bm, Cm, positions,
-                                                                               inv_freq, wB, wC, dB, dC, part);
+        by_lanes(s, [&](auto inter, auto lanes) {
+            norm_rotate_backward_kernel<T, decltype(inter)::value, decltype(lanes)::value>
+                <<<blocks, kThreads, 0, st>>>(s, dBo, dCo, Bm, Cm, positions, inv_freq, wB, wC, dB, dC, part);
+        });
     } else {
         norm_rotate_backward_any_kernel<T><<<blocks, kThreads, 0, st>>>(s, dBo, dCo, Bm, Cm, positions, inv_freq,
                                                                        wB, wC, dB, dC, part);
@@ -509,11 +603,10 @@ cudaError_t launch_norm_rotate(const RotateShape &s, bool bf16, const void *Bm, 
                                        inv_freq, wB, wC, static_cast<float *>(Bo), static_cast<float *>(Co), st);
 }
 
-// Blocks of the backward kernels; each leaves its share of the weights'
-// gradients.  Fewer than the forward pass's: a block's share costs 2 N values.
+// Blocks of the backward kernels; each leaves its share of the weights' gradients.
 int norm_rotate_backward_blocks(const RotateShape &s) {
     const int64_t per = kThreads / s.lanes, need = (s.tokens + per - 1) / per;
-    return int(need < kMostBlocks / 2 ? need : kMostBlocks / 2);
+    return int(even_blocks(need, kBackwardPerSm));
 }
 
 cudaError_t launch_norm_rotate_backward(const RotateShape &s, bool bf16, const void *dBo, const void *dCo,

@@ -11,7 +11,7 @@ struct RotateShape {
     int64_t tokens;                    // batch * T
     int64_t B_batch, B_token, C_batch, C_token;  // strides in elements
     int T, G, N, rotary;
-    int lanes;                         // lanes of a token: N / 8, up to a power of two
+    int lanes;                         // lanes of a token: N / 8, up to a power of two, 4 to 32
     int interleaved;
     float eps;
 };
