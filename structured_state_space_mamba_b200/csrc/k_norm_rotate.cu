@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 // blocks an SM holds, by the registers that they take without spilling
-template <typename T> constexpr int kForwardPerSm = sizeof(T) == 2 ? 6 : 5;
+template <typename T> constexpr int kForwardPerSm = sizeof(T) == 2 ? 7 : 5;
 constexpr int kBackwardPerSm = 4;
 
 // four values as they lie in memory, and as numbers
@@ -72,12 +72,12 @@ __device__ __forceinline__ void sincos_turn(float f, float &s, float &c) {
     }
 }
 
-// turns of a position: its fraction, rounded once to fp32
-__device__ __forceinline__ float turn_fraction(double pos, double turns) {
-    const double t = pos * turns;
+// turns of a position: the fraction, rounded once to fp32
+constexpr double kInvTwoPi = 0.15915494309189533577;
+__device__ __forceinline__ float turn_fraction(double pos, float freq) {
+    const double t = pos * (double(freq) * kInvTwoPi);
     return float(t - rint(t));
 }
-constexpr double kInvTwoPi = 0.15915494309189533577;
 
 // A lane's eight values, v[0 .. 3] in pairs of neighbours: where its two vectors of
 // four lie, and how they turn.
@@ -104,22 +104,21 @@ __device__ __forceinline__ Lane lane_of(const RotateShape &s, int q) {
     return l;
 }
 
-// Turns a position by frequency of a lane's four pairs, 4q + k in either order.
-__device__ __forceinline__ void lane_turns(const RotateShape &s, const float *inv_freq, int q, double (&turns)[4]) {
+// The frequencies of a lane's four pairs, 4q + k in either order.
+__device__ __forceinline__ void lane_freqs(const RotateShape &s, const float *inv_freq, int q, float (&freq)[4]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        turns[k] = 4 * q + k < s.rotary / 2 ? double(__ldg(inv_freq + 4 * q + k)) * kInvTwoPi : 0.0;
+    for (int k = 0; k < 4; ++k) freq[k] = 4 * q + k < s.rotary / 2 ? __ldg(inv_freq + 4 * q + k) : 0.f;
 }
 // Sines and cosines of a lane's pairs at a position: half-split, (0, 1) and (2, 3) as
 // they meet the values; interleaved, pair by pair.
 template <typename T, bool INTER>
 struct Turn {
     float2 cs[INTER ? 4 : 2], sn[INTER ? 4 : 2];
-    __device__ __forceinline__ void at(double pos, const double (&turns)[4]) {
+    __device__ __forceinline__ void at(double pos, const float (&freq)[4]) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float s, c;
-            sincos_turn<T>(turn_fraction(pos, turns[k]), s, c);
+            sincos_turn<T>(turn_fraction(pos, freq[k]), s, c);
             if (INTER) {
                 cs[k] = both(c);
                 sn[k] = make_float2(-s, s);
@@ -189,8 +188,8 @@ norm_rotate_kernel(const __grid_constant__ RotateShape s, const T *__restrict__ 
     constexpr int kPer = kThreads / LANES;  // tokens of a block at a time
     const int q = threadIdx.x % LANES;
     const Lane l = lane_of(s, q);
-    double turns[4];
-    lane_turns(s, inv_freq, q, turns);
+    float freq[4];
+    lane_freqs(s, inv_freq, q, freq);
     float2 wb[4], wc[4];
     lane_weights(wB, l, wb);
     lane_weights(wC, l, wc);
@@ -216,7 +215,7 @@ norm_rotate_kernel(const __grid_constant__ RotateShape s, const T *__restrict__ 
         };
         fetch(int(blockIdx.y) < s.G);
         Turn<T, INTER> turn;
-        turn.at(act ? double(__ldg(positions + tok)) : 0.0, turns);
+        turn.at(act ? double(__ldg(positions + tok)) : 0.0, freq);
         int64_t o = (tok * s.G + blockIdx.y) * s.N;
         for (int g = blockIdx.y; g < s.G; g += gridDim.y, o += step) {
             float2 b[4], c[4];
@@ -279,8 +278,8 @@ norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__re
     __shared__ float red[kWarps][2][256];
     const int q = threadIdx.x % LANES;
     const Lane l = lane_of(s, q);
-    double turns[4];
-    lane_turns(s, inv_freq, q, turns);
+    float freq[4];
+    lane_freqs(s, inv_freq, q, freq);
     float2 wb[4], wc[4], gb[4], gc[4];
     lane_weights(wB, l, wb);
     lane_weights(wC, l, wc);
@@ -294,7 +293,7 @@ norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__re
         if (act) token_place(s, tok, ob, oc);
         const T *xb = Bm + ob, *xc = Cm + oc;
         Turn<T, INTER> turn;
-        turn.at(act ? double(__ldg(positions + tok)) : 0.0, turns);
+        turn.at(act ? double(__ldg(positions + tok)) : 0.0, freq);
         int64_t o = tok * s.G * s.N;
         for (int g = 0; g < s.G; ++g, o += s.N, xb += s.N, xc += s.N) {
             typename Raw<T>::type raw[8] = {};
@@ -412,7 +411,7 @@ norm_rotate_any_kernel(const __grid_constant__ RotateShape s, const T *__restric
             int p, q;
             pair_of(s, j, p, q);
             float sn, cs;
-            sincos_turn<T>(turn_fraction(pos, double(__ldg(inv_freq + j)) * kInvTwoPi), sn, cs);
+            sincos_turn<T>(turn_fraction(pos, __ldg(inv_freq + j)), sn, cs);
             const float a = to_f32<T>(x[p]) * rstd * (wt ? __ldg(wt + p) : 1.f);
             const float b = to_f32<T>(x[q]) * rstd * (wt ? __ldg(wt + q) : 1.f);
             o[p] = from_f32<T>(a * cs - b * sn);
@@ -456,7 +455,7 @@ norm_rotate_backward_any_kernel(const __grid_constant__ RotateShape s, const T *
             int p, q;
             pair_of(s, j, p, q);
             float sn, cs;
-            sincos_turn<T>(turn_fraction(pos, double(__ldg(inv_freq + j)) * kInvTwoPi), sn, cs);
+            sincos_turn<T>(turn_fraction(pos, __ldg(inv_freq + j)), sn, cs);
             const float d0 = to_f32<T>(d[p]), d1 = to_f32<T>(d[q]), x0 = to_f32<T>(x[p]), x1 = to_f32<T>(x[q]);
             z0[k] = d0 * cs + d1 * sn;
             z1[k] = d1 * cs - d0 * sn;
