@@ -749,7 +749,7 @@ def norm_rotate(B, C, positions, inv_freq, weight_B=None, weight_C=None, eps=1e-
 
 
 def _norm_rotate(st, dims, B, C, positions, inv_freq, weight_B, weight_C):
-    Bo, Co = B.new_empty(B.shape), C.new_empty(C.shape)
+    Bo, Co = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (B, C))
     _check(load().ssd_norm_rotate(ctypes.byref(dims), B.data_ptr(), C.data_ptr(), positions.data_ptr(),
                                   inv_freq.data_ptr() or None, _ptr_or_none(weight_B), _ptr_or_none(weight_C),
                                   Bo.data_ptr(), Co.data_ptr(), st))

@@ -391,14 +391,28 @@ __device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N
             for (int a = 0; a < N; ++a)
                 copy_async<kBytes>(dst[a] + n * kRows * kGlrCols + lane * kVals, src[a] + (ok ? o : 0), ok ? kBytes : 0);
         }
-    } else {
+    } else if (sizeof(T) == 4) {  // rows of any length still are whole words
 #pragma unroll
-        for (int a = 0; a < N; ++a)
-#pragma unroll 8
+        for (int n = 0; n < kWarpVals / 32; ++n) {
+            const int id = n * 32 + lane, row = id / kGlrCols, v = id % kGlrCols;
+            const bool ok = row < ntok && c0 + v < C;
+            const int64_t o = ok ? t.base + (int64_t(warp * kTok + row) * C + v) : 0;
+#pragma unroll
+            for (int a = 0; a < N; ++a) copy_async<4>(dst[a] + id, src[a] + o, ok ? 4 : 0);
+        }
+    } else {
+        // single values, all of a tensor's on their way before the first is stored
+#pragma unroll
+        for (int a = 0; a < N; ++a) {
+            T held[kWarpVals / 32];
+#pragma unroll
             for (int n = 0; n < kWarpVals / 32; ++n) {
                 const int id = n * 32 + lane, row = id / kGlrCols, v = id % kGlrCols;
-                dst[a][id] = row < ntok && c0 + v < C ? src[a][t.base + int64_t(warp * kTok + row) * C + v] : T(0.f);
+                held[n] = row < ntok && c0 + v < C ? src[a][t.base + (int64_t(warp * kTok + row) * C + v)] : T(0.f);
             }
+#pragma unroll
+            for (int n = 0; n < kWarpVals / 32; ++n) dst[a][n * 32 + lane] = held[n];
+        }
     }
 }
 
