@@ -162,25 +162,26 @@ __device__ __forceinline__ void store2(T *p, float2 v, bool a0, bool a1) {
         if (a1) p[1] = from_f32<T>(v.y);
     }
 }
+// A warp's 64 values of one row into the n-th checkpoint: one block of it.  `edge`:
+// with blocks of the largest numbers and such as are not finite; otherwise says
+// whether this is one, whose codes are then wrong.
 template <bool VEC>
-__device__ __forceinline__ void store_code2(int8_t *p, int c0, int c1, bool a0, bool a1) {
-    if (VEC) {
-        if (a0) *reinterpret_cast<char2 *>(p) = make_char2(char(c0), char(c1));
-    } else {
-        if (a0) p[0] = int8_t(c0);
-        if (a1) p[1] = int8_t(c1);
-    }
-}
-
-// A warp's 64 values of one row into the n-th checkpoint: one block of it.
-template <bool VEC>
-__device__ __forceinline__ void pack_row(const GlrPacked &pk, int n, float2 v, int64_t at, int64_t block, int lane,
-                                         int c, int C) {
+__device__ __forceinline__ bool pack_row(const GlrPacked &pk, int n, float2 v, int64_t at, int64_t block, int lane,
+                                         int c, int C, bool edge) {
     const uint32_t e = pack8_exp(__reduce_max_sync(
         0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)));
     const float inv = pack8_inv(e);
-    store_code2<VEC>(pk.codes[n] + at, pack8_code(v.x, inv), pack8_code(v.y, inv), c < C, c + 1 < C);
+    const uint32_t c0 = edge ? uint32_t(pack8_code(v.x, inv)) : pack8_fast(v.x, inv);
+    const uint32_t c1 = edge ? uint32_t(pack8_code(v.y, inv)) : pack8_fast(v.y, inv);
+    int8_t *p = pk.codes[n] + at;
+    if (VEC) {
+        if (c < C) *reinterpret_cast<uint16_t *>(p) = uint16_t(__byte_perm(c0, c1, 0x0040));
+    } else {
+        if (c < C) p[0] = int8_t(c0);
+        if (c + 1 < C) p[1] = int8_t(c1);
+    }
     if (lane == 0) pk.exps[n][block] = uint8_t(e);
+    return e >= kPackEdge;
 }
 
 // ---------------------------------------------------------------------------
@@ -594,14 +595,21 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         if (PACK) {
             const int c = t.ct * kGlrCols + 2 * lane;
             const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
-            int64_t row = t.tok + warp * kTok, o = t.base + (int64_t(warp * kTok) * C + 2 * lane);
+            auto pack = [&](bool edge) {
+                int64_t block = (t.tok + warp * kTok) * cols8 + t.ct;
+                int64_t o = t.base + (int64_t(warp * kTok) * C + 2 * lane);
+                bool more = false;
 #pragma unroll
-            for (int j = 0; j < kTok; ++j, ++row, o += C) {
-                if (j >= ntok) break;
-                pack_row<VEC>(p.pk, 0, unpack2(st.x + j * kGlrCols + 2 * lane), o, row * cols8 + t.ct, lane, c, C);
-                pack_row<VEC>(p.pk, 1, unpack2(st.r + j * kGlrCols + 2 * lane), o, row * cols8 + t.ct, lane, c, C);
-                pack_row<VEC>(p.pk, 2, unpack2(st.i + j * kGlrCols + 2 * lane), o, row * cols8 + t.ct, lane, c, C);
-            }
+                for (int j = 0; j < kTok; ++j, block += cols8, o += C) {
+                    if (j >= ntok) break;
+                    const int at = j * kGlrCols + 2 * lane;
+                    more |= pack_row<VEC>(p.pk, 0, unpack2(st.x + at), o, block, lane, c, C, edge);
+                    more |= pack_row<VEC>(p.pk, 1, unpack2(st.r + at), o, block, lane, c, C, edge);
+                    more |= pack_row<VEC>(p.pk, 2, unpack2(st.i + at), o, block, lane, c, C, edge);
+                }
+                return more;
+            };
+            if (pack(false)) pack(true);
         }
         float2 e1[kTok], u[kTok], P = both(1.f), S = both(0.f);
 #pragma unroll
@@ -666,7 +674,7 @@ struct BwdPlan {
     struct Stage {
         In in[3][kWarpVals];
         T dy[kWarpVals];
-        uint32_t exps[PACK ? 3 : 1][PACK ? kTok : 4];  // the words that hold the exponent bytes
+        uint32_t exps[PACK ? 3 : 1][PACK ? kTok : 4];  // the words around the exponent bytes, then the steps
     };
     struct alignas(128) Smem {
         Stage stage[kStages][kWarps];
@@ -819,15 +827,20 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         const int ntok = t.ntok - warp * kTok;
         copy_wait<NS - 1>();
         __syncwarp();
-        const typename Plan::Stage &st = sm.stage[k % NS][warp];
+        typename Plan::Stage &st = sm.stage[k % NS][warp];
+        if constexpr (PACK) {
+            if (lane < 3 * kTok) {
+                const int n = lane / kTok, j = lane % kTok;
+                const uint32_t shift = 8 * (uint32_t((t.tok + warp * kTok + j) * cols8 + t.ct) & 3u);
+                st.exps[n][j] = __float_as_uint(pack8_step((st.exps[n][j] >> shift) & 255u));
+            }
+            __syncwarp();
+        }
         // x, r or i of token j of this warp
         auto input = [&](int n, int j) -> float2 {
             const int o = j * kGlrCols + 2 * lane;
             if constexpr (PACK) {
-                const uint32_t shift = 8 * uint32_t(((t.tok + warp * kTok + j) * cols8 + t.ct) & 3);
-                const float step = pack8_step((st.exps[n][j] >> shift) & 255u);
-                const char2 q = *reinterpret_cast<const char2 *>(st.in[n] + o);
-                return make_float2(float(q.x) * step, float(q.y) * step);
+                return unpack8_two(*reinterpret_cast<const uint16_t *>(st.in[n] + o), __uint_as_float(st.exps[n][j]));
             } else {
                 return unpack2(st.in[n] + o);
             }

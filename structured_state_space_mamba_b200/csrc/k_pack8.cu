@@ -87,9 +87,19 @@ pack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const T *__restrict__ x, 
         if (!ok[k]) continue;
         const uint32_t ex = pack8_exp(m);
         const float inv = pack8_inv(ex);
-        uint32_t w[2] = {0u, 0u};
+        uint32_t q[8];
+        if (ex < kPackEdge) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(pack8_code(v[k][e], inv) & 255) << (8 * (e & 3));
+            for (int e = 0; e < 8; ++e) q[e] = pack8_fast(v[k][e], inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = uint32_t(pack8_code(v[k][e], inv));
+        }
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[h] = __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040),
+                               __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040), 0x5410);
         *reinterpret_cast<uint2 *>(codes + o[k]) = make_uint2(w[0], w[1]);
         if (sub == 0) exps[n0 + k * kPer] = uint8_t(ex);
     }
@@ -120,7 +130,11 @@ unpack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const int8_t *__restric
         const float step = pack8_step(ex[k]);
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = float(int8_t((e < 4 ? q[k].x : q[k].y) >> (8 * (e & 3)))) * step;
+        for (int e = 0; e < 8; e += 2) {
+            const float2 two = unpack8_two((e < 4 ? q[k].x : q[k].y) >> (8 * (e & 2)), step);
+            v[e] = two.x;
+            v[e + 1] = two.y;
+        }
         store8(out + o[k], v);
     }
 }

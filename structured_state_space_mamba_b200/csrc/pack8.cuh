@@ -19,15 +19,16 @@ constexpr int kPackBlock = 64;
 // Exponent byte of a block from the bits of its largest magnitude (sign
 // cleared; a NaN's bits are above infinity's): the smallest e >= 1 with
 // max < 127.5 * 2^(e - 127), so that the largest code rounds to at most 127.
-// 127.5 = 1.9921875 * 2^6: the mantissa decides between E - 6 and E - 5.  At most
-// 248 (64 steps of the next one are past the largest float): there alone codes
-// saturate.  255 for a block with an infinity or a NaN.
+// 127.5 = 1.9921875 * 2^6, so e is the exponent less 6, after a carry out of
+// mantissas from .9921875 (0x7f0000) up.  At most 248 (64 steps of the next one
+// are past the largest float): there alone codes saturate.  255 for a block with
+// an infinity or a NaN.
 __device__ __forceinline__ uint32_t pack8_exp(uint32_t maxbits) {
-    const uint32_t E = maxbits >> 23;
-    const uint32_t up = (maxbits & 0x7fffffu) >= 0x7f0000u ? 5u : 6u;
-    const uint32_t e = E > up ? E - up : 1u;
-    return E == 255u ? 255u : min(e, 248u);
+    const int e = min(max(int((maxbits + 0x10000u) >> 23) - 6, 1), 248);
+    return maxbits >= 0x7f800000u ? 255u : uint32_t(e);
 }
+// Blocks from this byte on need pack8_code(); the others may take pack8_fast().
+constexpr uint32_t kPackEdge = 248;
 // 1 / step as a float (0 for the byte 255: every code of such a block is 0)
 __device__ __forceinline__ float pack8_inv(uint32_t e) {
     return __uint_as_float(e == 255u ? 0u : (254u - e) << 23);
@@ -39,6 +40,20 @@ __device__ __forceinline__ float pack8_step(uint32_t e) { return __uint_as_float
 // smallest step.  An infinity or NaN times 0 is NaN, which converts to 0.
 __device__ __forceinline__ int pack8_code(float v, float inv) {
     return min(max(__float2int_rn(v * inv), -127), 127);
+}
+// The same in the low byte, below kPackEdge: adding 1.5 * 2^23 rounds to a whole
+// number, ties to even, and leaves it in the low bits.  The conversion to an
+// integer runs at a quarter of the rate, on the unit that the exponentials need.
+__device__ __forceinline__ uint32_t pack8_fast(float v, float inv) {
+    return __float_as_uint(fmaf(v, inv, 12582912.f));
+}
+// Two codes (the low bytes of a word) as numbers: a byte with its sign bit flipped,
+// in the mantissa of 2^23, is 8388736 + code.  Without conversions for the same
+// reason.
+__device__ __forceinline__ float2 unpack8_two(uint32_t w, float step) {
+    const uint32_t u = w ^ 0x8080u;
+    return make_float2((__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - 8388736.f) * step,
+                       (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - 8388736.f) * step);
 }
 
 }  // namespace ssd
