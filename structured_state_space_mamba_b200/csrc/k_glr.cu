@@ -162,26 +162,55 @@ __device__ __forceinline__ void store2(T *p, float2 v, bool a0, bool a1) {
         if (a1) p[1] = from_f32<T>(v.y);
     }
 }
-// A warp's 64 values of one row into the n-th checkpoint: one block of it.  `edge`:
-// with blocks of the largest numbers and such as are not finite; otherwise says
-// whether this is one, whose codes are then wrong.
-template <bool VEC>
-__device__ __forceinline__ bool pack_row(const GlrPacked &pk, int n, float2 v, int64_t at, int64_t block, int lane,
-                                         int c, int C, bool edge) {
+// A warp's 64 values of one row into the n-th checkpoint, one block of it, two
+// values a lane: rows of any length.
+__device__ __forceinline__ void pack_row(const GlrPacked &pk, int n, float2 v, int64_t at, int64_t block, int lane,
+                                         int c, int C) {
     const uint32_t e = pack8_exp(__reduce_max_sync(
         0xffffffffu, max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu)));
     const float inv = pack8_inv(e);
-    const uint32_t c0 = edge ? uint32_t(pack8_code(v.x, inv)) : pack8_fast(v.x, inv);
-    const uint32_t c1 = edge ? uint32_t(pack8_code(v.y, inv)) : pack8_fast(v.y, inv);
-    int8_t *p = pk.codes[n] + at;
-    if (VEC) {
-        if (c < C) *reinterpret_cast<uint16_t *>(p) = uint16_t(__byte_perm(c0, c1, 0x0040));
-    } else {
-        if (c < C) p[0] = int8_t(c0);
-        if (c + 1 < C) p[1] = int8_t(c1);
-    }
+    if (c < C) pk.codes[n][at] = int8_t(pack8_code(v.x, inv));
+    if (c + 1 < C) pk.codes[n][at + 1] = int8_t(pack8_code(v.y, inv));
     if (lane == 0) pk.exps[n][block] = uint8_t(e);
-    return e >= kPackEdge;
+}
+// Four rows at once, eight values a lane, eight lanes a block: a third of the
+// instructions.  `from`: the lane's eight values in shared memory.
+template <typename T>
+__device__ __forceinline__ void pack_four(const T *from, int8_t *codes, uint8_t *exps, bool a0, bool a1, bool lead) {
+    float v[8];
+    uint32_t m;
+    if constexpr (sizeof(T) == 2) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(from);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        m = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
+                     __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = max(m & 0xffff0000u, m << 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(u[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        }
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(from), b = *reinterpret_cast<const float4 *>(from + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    const uint32_t ex = pack8_exp(m);
+    const uint2 q = pack8_eight(v, ex);
+    if (sizeof(T) == 2) {  // rows are whole eights
+        if (a0) *reinterpret_cast<uint2 *>(codes) = q;
+    } else {
+        if (a0) reinterpret_cast<uint32_t *>(codes)[0] = q.x;
+        if (a1) reinterpret_cast<uint32_t *>(codes)[1] = q.y;
+    }
+    if (lead && a0) *exps = uint8_t(ex);
 }
 
 // ---------------------------------------------------------------------------
@@ -593,23 +622,31 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         __syncwarp();
         const typename Plan::Stage &st = sm.stage[k % NS][warp];
         if (PACK) {
-            const int c = t.ct * kGlrCols + 2 * lane;
             const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
-            auto pack = [&](bool edge) {
+            if constexpr (VEC) {
+#pragma unroll
+                for (int h = 0; h < kTok / 4; ++h) {
+                    const int j = 4 * h + lane / 8, v = lane % 8 * 8, c = t.ct * kGlrCols + v;
+                    const bool a0 = j < ntok && c < C, a1 = j < ntok && c + 4 < C;
+                    const int64_t o = t.base + (int64_t(warp * kTok + j) * C + v);
+                    const int64_t block = (t.tok + warp * kTok + j) * cols8 + t.ct;
+                    pack_four(st.x + j * kGlrCols + v, p.pk.codes[0] + o, p.pk.exps[0] + block, a0, a1, v == 0);
+                    pack_four(st.r + j * kGlrCols + v, p.pk.codes[1] + o, p.pk.exps[1] + block, a0, a1, v == 0);
+                    pack_four(st.i + j * kGlrCols + v, p.pk.codes[2] + o, p.pk.exps[2] + block, a0, a1, v == 0);
+                }
+            } else {
+                const int c = t.ct * kGlrCols + 2 * lane;
                 int64_t block = (t.tok + warp * kTok) * cols8 + t.ct;
                 int64_t o = t.base + (int64_t(warp * kTok) * C + 2 * lane);
-                bool more = false;
 #pragma unroll
                 for (int j = 0; j < kTok; ++j, block += cols8, o += C) {
                     if (j >= ntok) break;
                     const int at = j * kGlrCols + 2 * lane;
-                    more |= pack_row<VEC>(p.pk, 0, unpack2(st.x + at), o, block, lane, c, C, edge);
-                    more |= pack_row<VEC>(p.pk, 1, unpack2(st.r + at), o, block, lane, c, C, edge);
-                    more |= pack_row<VEC>(p.pk, 2, unpack2(st.i + at), o, block, lane, c, C, edge);
+                    pack_row(p.pk, 0, unpack2(st.x + at), o, block, lane, c, C);
+                    pack_row(p.pk, 1, unpack2(st.r + at), o, block, lane, c, C);
+                    pack_row(p.pk, 2, unpack2(st.i + at), o, block, lane, c, C);
                 }
-                return more;
-            };
-            if (pack(false)) pack(true);
+            }
         }
         float2 e1[kTok], u[kTok], P = both(1.f), S = both(0.f);
 #pragma unroll

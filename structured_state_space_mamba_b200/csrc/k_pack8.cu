@@ -86,21 +86,7 @@ pack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const T *__restrict__ x, 
         for (int s = 4; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
         if (!ok[k]) continue;
         const uint32_t ex = pack8_exp(m);
-        const float inv = pack8_inv(ex);
-        uint32_t q[8];
-        if (ex < kPackEdge) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = pack8_fast(v[k][e], inv);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = uint32_t(pack8_code(v[k][e], inv));
-        }
-        uint32_t w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[h] = __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040),
-                               __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040), 0x5410);
-        *reinterpret_cast<uint2 *>(codes + o[k]) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(codes + o[k]) = pack8_eight(v[k], ex);
         if (sub == 0) exps[n0 + k * kPer] = uint8_t(ex);
     }
 }

@@ -47,6 +47,20 @@ __device__ __forceinline__ int pack8_code(float v, float inv) {
 __device__ __forceinline__ uint32_t pack8_fast(float v, float inv) {
     return __float_as_uint(fmaf(v, inv, 12582912.f));
 }
+// Eight values of a block as codes.
+__device__ __forceinline__ uint2 pack8_eight(const float (&v)[8], uint32_t ex) {
+    const float inv = pack8_inv(ex);
+    uint32_t q[8];
+    if (ex < kPackEdge) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = pack8_fast(v[e], inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = uint32_t(pack8_code(v[e], inv));
+    }
+    return make_uint2(__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+}
 // Two codes (the low bytes of a word) as numbers: a byte with its sign bit flipped,
 // in the mantissa of 2^23, is 8388736 + code.  Without conversions for the same
 // reason.
