@@ -405,6 +405,19 @@ SSD_API ssd_status_t ssd_unpack8(int64_t rows, int64_t cols, int dtype, const ss
                                  void *out, void *stream);
 
 /*
+ * ssd_backward_packed8 -- ssd_backward from the 8-bit checkpoints of x, Bm and Cm
+ * (`packed`: three, in that order) in place of the tensors themselves: x as
+ * rows of headdim values (B T H of them), Bm and Cm as rows of dstate values (B T G).
+ * The gradients at the values that the checkpoints stand for; everything else as
+ * for ssd_backward, with dims->dtype the type of dy and of dx, dB, dC.
+ */
+SSD_API ssd_status_t ssd_backward_packed8(const ssd_dims_t *dims, const ssd_packed8_t *packed, const float *dt,
+                                          const float *A, const float *D, int chunk_len,
+                                          const float *init_state, const void *dy, const float *dfinal_state,
+                                          void *dx, float *ddt, float *dA, void *dB, void *dC, float *dD,
+                                          float *dinit_state, void *stream);
+
+/*
  * ssd_glr_forward -- the recurrence over whole sequences.
  *
  *   cu_seqlens  NULL: every row of the batch is one sequence.  Else a HOST

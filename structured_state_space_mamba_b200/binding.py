@@ -25,7 +25,7 @@ EXPORTS = ("ssd_forward", "ssd_forward_ws", "ssd_forward_stage", "ssd_workspace_
            "ssd_forward_static", "ssd_step", "ssd_forward_block", "ssd_block_workspace_bytes",
            "ssd_forward_varlen", "ssd_varlen_workspace_bytes", "ssd_backward", "ssd_workspace_trim",
            "ssd_glr_forward", "ssd_glr_backward", "ssd_glr_step", "ssd_glr_chunk_rows", "ssd_pack8", "ssd_unpack8",
-           "ssd_norm_rotate", "ssd_norm_rotate_backward")
+           "ssd_norm_rotate", "ssd_norm_rotate_backward", "ssd_backward_packed8")
 STAGES = ("ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan")
 
 
@@ -151,7 +151,9 @@ def load():
     lib.ssd_unpack8.argtypes = [i64, i64, ctypes.c_int, packed_p, vp, vp]
     lib.ssd_norm_rotate.argtypes = [rot_p, vp, vp, vp, fp, fp, fp, vp, vp, vp]
     lib.ssd_norm_rotate_backward.argtypes = [rot_p, vp, vp, vp, vp, vp, fp, fp, fp, vp, vp, fp, fp, vp]
-    for f in (lib.ssd_glr_forward, lib.ssd_glr_backward, lib.ssd_glr_step, lib.ssd_pack8, lib.ssd_unpack8,
+    lib.ssd_backward_packed8.argtypes = [dims_p, packed_p, fp, fp, fp, ctypes.c_int, fp, vp, fp, vp, fp, fp, vp, vp,
+                                         fp, fp, vp]
+    for f in (lib.ssd_backward_packed8, lib.ssd_glr_forward, lib.ssd_glr_backward, lib.ssd_glr_step, lib.ssd_pack8, lib.ssd_unpack8,
               lib.ssd_norm_rotate, lib.ssd_norm_rotate_backward):
         f.restype = ctypes.c_int
     _lib = lib
@@ -512,7 +514,8 @@ def _launch(index, stream, call, *args):
     if stream is not None:
         handle = int(getattr(stream, "cuda_stream", stream))
         if handle != current:
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=index)):
+            other = torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
+            with torch.cuda.stream(other):
                 return call(handle, *args)
     return call(current, *args)
 
@@ -584,6 +587,45 @@ def _unpack8(st, packed, dtype, out):
     return out
 
 
+def backward_packed8(x, dt, A, B, C, dy, D=None, chunk_len=256, init_state=None, dfinal_state=None, stream=None):
+    """``backward`` from 8-bit checkpoints (``pack8``) of x, B and C through
+    ``ssd_backward_packed8``: the gradients at the values that they stand for,
+    in dy's dtype.  Returns the dict of ``backward``."""
+    code, index = _storage("dy", dy)
+    if dy.dim() != 4:
+        raise ValueError("dy must be [batch, seqlen, nheads, headdim]")
+    for name, p in (("x", x), ("B", B), ("C", C)):
+        if not isinstance(p, Packed8):
+            raise ValueError(f"{name} must be a Packed8")
+    bsz, T, H, P = dy.shape
+    if B.codes.dim() != 4:
+        raise ValueError("B and C must be [batch, seqlen, ngroups, dstate]")
+    G, N = B.shape[2:]
+    _need("dy", dy, index, dy.dtype, dy.shape)
+    x._check("x", index, dy.shape)
+    B._check("B", index, (bsz, T, G, N))
+    C._check("C", index, (bsz, T, G, N))
+    for name, t, shape in (("dt", dt, (bsz, T, H)), ("A", A, (H,)), ("D", D, (H,)),
+                           ("init_state", init_state, (bsz, H, P, N)),
+                           ("dfinal_state", dfinal_state, (bsz, H, P, N))):
+        if t is not None:
+            _need(name, t, index, torch.float32, shape)
+    return _launch(index, stream, _backward_packed8, Dims(bsz, T, H, P, N, G, code, 0), x, dt, A, B, C, dy, D,
+                   int(chunk_len), init_state, dfinal_state)
+
+
+def _backward_packed8(st, dims, x, dt, A, B, C, dy, D, chunk_len, init_state, dfinal_state):
+    out = dict(dx=torch.empty_like(dy), ddt=torch.empty_like(dt), dA=torch.empty_like(A),
+               dB=dy.new_empty(B.shape), dC=dy.new_empty(C.shape), dD=None if D is None else torch.empty_like(D),
+               dinit_state=None if init_state is None else torch.empty_like(init_state))
+    pk = (_Packed8 * 3)(x._c(), B._c(), C._c())
+    _check(load().ssd_backward_packed8(
+        ctypes.byref(dims), pk, dt.data_ptr(), A.data_ptr(), _ptr_or_none(D), chunk_len, _ptr_or_none(init_state),
+        dy.data_ptr(), _ptr_or_none(dfinal_state), out["dx"].data_ptr(), out["ddt"].data_ptr(), out["dA"].data_ptr(),
+        out["dB"].data_ptr(), out["dC"].data_ptr(), _ptr_or_none(out["dD"]), _ptr_or_none(out["dinit_state"]), st))
+    return out
+
+
 class GlrSaved:
     """What ``glr_forward`` keeps for ``glr_backward``: the inputs, or their 8-bit
     checkpoints, and the state entering every 64 tokens of every sequence."""
@@ -641,7 +683,8 @@ def _glr_forward(st, dims, x, r, i, A, init_state, cu, rows, return_final_state,
                                _ptr_or_none(states), pk, st))
     if save is None:
         return (y, final) if return_final_state else y
-    saved = GlrSaved(*(packed or (x, r, i)), A, states, cu, rows)
+    # the offsets are kept too: a copy, as they may be the caller's own array
+    saved = GlrSaved(*(packed or (x, r, i)), A, states, None if cu is None else cu.copy(), rows)
     return (y, final, saved) if return_final_state else (y, saved)
 
 

@@ -5,7 +5,7 @@
 // Eight lanes take a block of 64 values, 16 or 32 bytes a lane in one or two
 // vectors, and find its largest magnitude by shuffles; a thread has kUnroll
 // blocks' loads in flight.  Rows that are no whole number of 8-value vectors go
-// one warp a block with single-value accesses.
+// a warp a block with single-value accesses, eight blocks in flight.
 #include "common.cuh"
 #include "glr.h"
 #include "pack8.cuh"
@@ -45,18 +45,47 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Where a lane's eight values of block n lie (n = row * nb + block of the row);
-// false behind the row's end.  FLAT: whole blocks only, rows follow each other.
+// Where a lane's eight values of its blocks lie: the first by a division, the next
+// ones, kThreads / 8 blocks on, by steps of whole rows and blocks of a row.  FLAT:
+// whole blocks only, rows follow each other.
 template <bool FLAT>
-__device__ __forceinline__ bool place(int64_t n, int64_t nb, int64_t cols, int sub, int64_t &o) {
-    if (FLAT) {
-        o = n * kPackBlock + sub * 8;
-        return true;
+struct Place {
+    int64_t row, c, rows_on, blocks_on, nb, cols;
+    int sub;
+    __device__ __forceinline__ Place(int64_t n, int64_t nb_, int64_t cols_, int sub_)
+        : nb(nb_), cols(cols_), sub(sub_) {
+        if (FLAT) {
+            row = n;
+        } else {
+            row = n / nb;
+            c = n - row * nb;
+            rows_on = (kThreads / 8) / nb;
+            blocks_on = (kThreads / 8) - rows_on * nb;
+        }
     }
-    const int64_t row = n / nb, c = (n - row * nb) * kPackBlock + sub * 8;
-    o = row * cols + c;
-    return c < cols;
-}
+    // the place; false behind the row's end
+    __device__ __forceinline__ bool at(int64_t &o) const {
+        if (FLAT) {
+            o = row * kPackBlock + sub * 8;
+            return true;
+        }
+        const int64_t v = c * kPackBlock + sub * 8;
+        o = row * cols + v;
+        return v < cols;
+    }
+    __device__ __forceinline__ void on() {
+        if (FLAT) {
+            row += kThreads / 8;
+        } else {
+            row += rows_on;
+            c += blocks_on;
+            if (c >= nb) {
+                c -= nb;
+                ++row;
+            }
+        }
+    }
+};
 
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kThreads)
@@ -68,10 +97,11 @@ pack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const T *__restrict__ x, 
     float v[kUnroll][8];
     int64_t o[kUnroll];
     bool ok[kUnroll];
+    Place<FLAT> place(n0, nb, cols, sub);
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kUnroll; ++k, place.on()) {
         const int64_t n = n0 + k * kPer;
-        ok[k] = n < blocks && place<FLAT>(n, nb, cols, sub, o[k]);
+        ok[k] = place.at(o[k]) && n < blocks;
         if (ok[k]) load8(x + o[k], v[k]);
         else
 #pragma unroll
@@ -102,10 +132,11 @@ unpack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const int8_t *__restric
     uint32_t ex[kUnroll];
     int64_t o[kUnroll];
     bool ok[kUnroll];
+    Place<FLAT> place(n0, nb, cols, sub);
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
+    for (int k = 0; k < kUnroll; ++k, place.on()) {
         const int64_t n = n0 + k * kPer;
-        ok[k] = n < blocks && place<FLAT>(n, nb, cols, sub, o[k]);
+        ok[k] = place.at(o[k]) && n < blocks;
         if (!ok[k]) continue;
         q[k] = __ldg(reinterpret_cast<const uint2 *>(codes + o[k]));
         ex[k] = __ldg(exps + n);
@@ -125,36 +156,74 @@ unpack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const int8_t *__restric
     }
 }
 
-// any row length: one warp a block, lanes at a stride of 32 values
+// any row length: a warp takes kRun blocks in a row, all of their loads on their way
+// before the first is used, lanes at a stride of 32 values
+constexpr int kRun = 8;
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 pack8_any_kernel(int64_t blocks, int64_t nb, int64_t cols, const T *__restrict__ x, int8_t *__restrict__ codes,
                  uint8_t *__restrict__ exps) {
     const int lane = threadIdx.x & 31;
-    const int64_t n = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (n >= blocks) return;
-    const int64_t row = n / nb, c = (n - row * nb) * kPackBlock + lane, o = row * cols + c;
-    const bool a = c < cols, b = c + 32 < cols;
-    const float v = a ? to_f32<T>(x[o]) : 0.f, w = b ? to_f32<T>(x[o + 32]) : 0.f;
-    const uint32_t m = __reduce_max_sync(0xffffffffu, max(__float_as_uint(v) & 0x7fffffffu,
-                                                          __float_as_uint(w) & 0x7fffffffu));
-    const uint32_t ex = pack8_exp(m);
-    const float inv = pack8_inv(ex);
-    if (a) codes[o] = int8_t(pack8_code(v, inv));
-    if (b) codes[o + 32] = int8_t(pack8_code(w, inv));
-    if (lane == 0) exps[n] = uint8_t(ex);
+    const int64_t n0 = (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRun;
+    if (n0 >= blocks) return;
+    int64_t row = n0 / nb, c = (n0 - row * nb) * kPackBlock;
+    float v[kRun][2];
+    int64_t o[kRun];
+    int left[kRun];  // values of the row from the block's first on, as far as they matter
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        o[k] = row * cols + c + lane;
+        left[k] = n0 + k < blocks ? int(min(cols - c, int64_t(kPackBlock))) : 0;
+        v[k][0] = lane < left[k] ? to_f32<T>(x[o[k]]) : 0.f;
+        v[k][1] = lane + 32 < left[k] ? to_f32<T>(x[o[k] + 32]) : 0.f;
+        c += kPackBlock;
+        if (c >= cols) {
+            c = 0;
+            ++row;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        if (left[k] == 0) break;
+        const uint32_t ex = pack8_exp(__reduce_max_sync(
+            0xffffffffu, max(__float_as_uint(v[k][0]) & 0x7fffffffu, __float_as_uint(v[k][1]) & 0x7fffffffu)));
+        const float inv = pack8_inv(ex);
+        if (lane < left[k]) codes[o[k]] = int8_t(pack8_code(v[k][0], inv));
+        if (lane + 32 < left[k]) codes[o[k] + 32] = int8_t(pack8_code(v[k][1], inv));
+        if (lane == 0) exps[n0 + k] = uint8_t(ex);
+    }
 }
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 unpack8_any_kernel(int64_t blocks, int64_t nb, int64_t cols, const int8_t *__restrict__ codes,
                    const uint8_t *__restrict__ exps, T *__restrict__ out) {
     const int lane = threadIdx.x & 31;
-    const int64_t n = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (n >= blocks) return;
-    const int64_t row = n / nb, c = (n - row * nb) * kPackBlock + lane, o = row * cols + c;
-    const float step = pack8_step(exps[n]);
-    if (c < cols) out[o] = from_f32<T>(float(codes[o]) * step);
-    if (c + 32 < cols) out[o + 32] = from_f32<T>(float(codes[o + 32]) * step);
+    const int64_t n0 = (int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kRun;
+    if (n0 >= blocks) return;
+    int64_t row = n0 / nb, c = (n0 - row * nb) * kPackBlock;
+    int8_t q[kRun][2];
+    uint32_t ex[kRun];
+    int64_t o[kRun];
+    int left[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        o[k] = row * cols + c + lane;
+        left[k] = n0 + k < blocks ? int(min(cols - c, int64_t(kPackBlock))) : 0;
+        q[k][0] = lane < left[k] ? codes[o[k]] : int8_t(0);
+        q[k][1] = lane + 32 < left[k] ? codes[o[k] + 32] : int8_t(0);
+        ex[k] = left[k] ? exps[n0 + k] : 1u;
+        c += kPackBlock;
+        if (c >= cols) {
+            c = 0;
+            ++row;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+        const float step = pack8_step(ex[k]);
+        if (lane < left[k]) out[o[k]] = from_f32<T>(float(q[k][0]) * step);
+        if (lane + 32 < left[k]) out[o[k] + 32] = from_f32<T>(float(q[k][1]) * step);
+    }
 }
 
 struct Plan {
@@ -166,9 +235,9 @@ Plan plan_of(int64_t rows, int64_t cols) {
     Plan p;
     p.nb = (cols + kPackBlock - 1) / kPackBlock;
     p.blocks = rows * p.nb;
-    const int64_t per = kThreads / 8 * kUnroll, any = kThreads / 32;
+    const int64_t per = kThreads / 8 * kUnroll, any = kThreads / 32 * kRun;
     const int64_t g = (p.blocks + per - 1) / per, h = (p.blocks + any - 1) / any;
-    p.fits = h <= 0x7fffffff;
+    p.fits = g <= 0x7fffffff && h <= 0x7fffffff;
     p.vec_grid = unsigned(g);
     p.any_grid = unsigned(h);
     return p;

@@ -696,14 +696,25 @@ ssd_status_t ssd_forward_varlen(const ssd_dims_t *dims, const int64_t *cu_seqlen
 // backward: the reverse mode, through four fp32 scans of the forward plans and
 // the element-wise / prefix kernels of k_backward.cu
 // ---------------------------------------------------------------------------
-ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const float *dt, const float *A, const void *Bm,
-                          const void *Cm, const float *D, int chunk_len, const float *init_state, const void *dy,
-                          const float *dfinal_state, void *dx, float *ddt, float *dA, void *dB, void *dC,
-                          float *dD, float *dinit_state, void *stream) {
+}  // extern "C"
+
+namespace {
+
+// x, Bm and Cm, or (all three null) their 8-bit checkpoints in that order, which are
+// read back into the scratch first
+ssd_status_t backward(const ssd_dims_t *dims, const void *x, const float *dt, const float *A, const void *Bm,
+                      const void *Cm, const ssd_packed8_t *packed, const float *D, int chunk_len,
+                      const float *init_state, const void *dy, const float *dfinal_state, void *dx, float *ddt,
+                      float *dA, void *dB, void *dC, float *dD, float *dinit_state, void *stream) {
     Plan pf;
     ssd_status_t s = make_plan(dims, chunk_len, &pf);
     if (s != SSD_OK) return s;
-    if (!x || !dt || !A || !Bm || !Cm || !dy || !dx || !ddt || !dA || !dB || !dC) return SSD_ERR_NULL_ARG;
+    if (!packed && (!x || !Bm || !Cm)) return SSD_ERR_NULL_ARG;
+    if (!dt || !A || !dy || !dx || !ddt || !dA || !dB || !dC) return SSD_ERR_NULL_ARG;
+    for (int n = 0; packed && n < 3; ++n) {
+        if (!packed[n].codes || !packed[n].exps) return SSD_ERR_NULL_ARG;
+        if (misaligned(packed[n].codes) || misaligned(packed[n].exps)) return SSD_ERR_MISALIGNED;
+    }
     if (dims->nheads > kMaxBackwardHeads) return SSD_ERR_UNSUPPORTED;
     {
         const void *ptrs[] = {x, dt, A, Bm, Cm, D, init_state, dy, dfinal_state, dx, ddt, dA, dB, dC, dD,
@@ -766,6 +777,9 @@ ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const float *dt
     const size_t o_xu = take(ntok * 4), o_cc = take(ntok * 4), o_rr = take(ntok * 4), o_dd = take(ntok * 4),
                  o_R0 = take(nbh * 4), o_dAp = take(nbh * 4), o_dDp = take(nbh * 4);
     const size_t o_ft = dfinal_state ? take(nst * 4) : 0, o_ht = init_state ? take(nst * 4) : 0;
+    const size_t esz = bf16 ? 2 : 4;
+    const size_t o_px = packed ? take(nx * esz) : 0, o_pb = packed ? take(nbc * esz) : 0,
+                 o_pc = packed ? take(nbc * esz) : 0;
     const size_t o_ws = off;
     off = align_up(off + (pk.ws.total_bytes > pt.ws.total_bytes ? pk.ws.total_bytes : pt.ws.total_bytes));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -789,14 +803,27 @@ ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const float *dt
     w.scan_bf16 = scan_bf16;
     float *ft = dfinal_state ? F(o_ft) : nullptr, *ht = init_state ? F(o_ht) : nullptr;
     char *ws = buf + o_ws;
+    s = SSD_OK;
+    if (packed) {
+        const int64_t tokens = a.batch * a.seqlen;
+        const struct { size_t at; int64_t rows, cols; } in[3] = {{o_px, tokens * a.nheads, a.headdim},
+                                                                 {o_pb, tokens * a.ngroups, a.dstate},
+                                                                 {o_pc, tokens * a.ngroups, a.dstate}};
+        for (int n = 0; n < 3 && s == SSD_OK; ++n)
+            if (ssd::launch_unpack8(in[n].rows, in[n].cols, bf16, packed[n].codes, packed[n].exps, V(in[n].at), st) !=
+                cudaSuccess)
+                s = SSD_ERR_CUDA;
+        x = V(o_px);
+        Bm = V(o_pb);
+        Cm = V(o_pc);
+    }
     // the forward-direction scans read the inputs themselves where their dtype fits
     const void *xs = copies ? static_cast<const void *>(w.xf) : x;    // the fp32 scan of h
     const void *bs = copies ? static_cast<const void *>(w.bf) : Bm;
     const void *cs = copies ? static_cast<const void *>(w.cf) : Cm;
     const void *xt = scan_bf16 || !bf16 ? x : static_cast<const void *>(w.xf);  // the transposed scans
     const void *dyt = dy_copy ? static_cast<const void *>(w.dyf) : dy;
-    s = SSD_OK;
-    if (ssd::launch_backward_prep(d, bf16, x, dy, dt, A, Bm, Cm, w, st) != cudaSuccess) s = SSD_ERR_CUDA;
+    if (s == SSD_OK && ssd::launch_backward_prep(d, bf16, x, dy, dt, A, Bm, Cm, w, st) != cudaSuccess) s = SSD_ERR_CUDA;
     if (s == SSD_OK && ft &&
         ssd::launch_transpose_state(int64_t(nbh), int(a.headdim), int(a.dstate), W, dfinal_state, ft, st) !=
             cudaSuccess)
@@ -823,6 +850,27 @@ ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const float *dt
         s = SSD_ERR_CUDA;
     if (cudaFreeAsync(buf, st) != cudaSuccess && s == SSD_OK) s = SSD_ERR_CUDA;
     return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const float *dt, const float *A, const void *Bm,
+                          const void *Cm, const float *D, int chunk_len, const float *init_state, const void *dy,
+                          const float *dfinal_state, void *dx, float *ddt, float *dA, void *dB, void *dC,
+                          float *dD, float *dinit_state, void *stream) {
+    return backward(dims, x, dt, A, Bm, Cm, nullptr, D, chunk_len, init_state, dy, dfinal_state, dx, ddt, dA, dB, dC,
+                    dD, dinit_state, stream);
+}
+
+ssd_status_t ssd_backward_packed8(const ssd_dims_t *dims, const ssd_packed8_t *packed, const float *dt,
+                                  const float *A, const float *D, int chunk_len, const float *init_state,
+                                  const void *dy, const float *dfinal_state, void *dx, float *ddt, float *dA,
+                                  void *dB, void *dC, float *dD, float *dinit_state, void *stream) {
+    if (!packed) return SSD_ERR_NULL_ARG;
+    return backward(dims, nullptr, dt, A, nullptr, nullptr, packed, D, chunk_len, init_state, dy, dfinal_state, dx,
+                    ddt, dA, dB, dC, dD, dinit_state, stream);
 }
 
 const char *ssd_status_string(ssd_status_t status) {

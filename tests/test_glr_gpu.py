@@ -114,7 +114,8 @@ def test_packed_sequences(oracle, cu, dtype, C):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape,cu", [((2, 70, 64), None), ((1, 200, 130), None), ((1, 130, 67), [0, 1, 1, 66, 130]),
-                                      ((3, 1, 5), None)])
+                                      ((3, 1, 5), None), ((2, 65, 36), None), ((1, 128, 200), [0, 64, 128]),
+                                      ((1, 3, 1), None)])
 def test_saved_in_8_bits(oracle, shape, cu, dtype):
     """The checkpoints that the forward pass writes are pack8's; the backward pass
     is the gradient at the values they stand for, from the kept states."""
@@ -215,6 +216,26 @@ def test_same_bits_every_time_and_on_two_streams():
     assert binding.device_status() == 0
 
 
+def test_streams_by_object_and_handle():
+    """The default stream from another one, a torch stream and its handle; the offsets
+    given to the forward pass may change before the backward one."""
+    p = problem((1, 300, 64), "f32", seed=12, S=2)
+    cu = np.array([0, 100, 300])
+    args = (p["x"], p["r"], p["i"], p["A"])
+    want, saved = binding.glr_forward(*args, cu_seqlens=cu, save="inputs")
+    g = binding.glr_backward(p["dy"], saved)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = [binding.glr_forward(*args, cu_seqlens=cu, stream=t) for t in (0, None, s, s.cuda_stream)]
+    y, kept = binding.glr_forward(*args, cu_seqlens=cu, save="inputs")
+    cu[1] = 200
+    again = binding.glr_backward(p["dy"], kept)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want) for t in got + [y])
+    assert all(torch.equal(again[k], g[k]) for k in ("dx", "dr", "di", "dA"))
+
+
 def test_captured_and_replayed():
     """Two graphs of the whole training step, replayed in turn on other inputs."""
     p = problem((2, 500, 96), "bf16", seed=13)
@@ -261,3 +282,56 @@ def test_out_and_untouched_neighbours(oracle):
     assert y.data_ptr() == out.data_ptr()
     assert (big[:32] == 7).all() and (big[32 + T:] == 7).all()
     assert torch.equal(y, binding.glr_forward(p["x"], p["r"], p["i"], p["A"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [128, 37])
+def test_checkpoints_of_values_at_the_edge(dtype, C):
+    """Infinities, NaN, zeros and the largest numbers among the inputs: the forward
+    pass writes the checkpoints that pack8 writes."""
+    p = problem((1, 40, C), dtype, seed=17)
+    top = torch.finfo(TYPES[dtype]).max
+    for k, v in (("x", top), ("r", float("inf")), ("i", float("nan"))):
+        p[k][0, 3, 1], p[k][0, 9, C - 1], p[k][0, 20] = v, -v, 0
+    _, saved = binding.glr_forward(p["x"], p["r"], p["i"], p["A"], save="packed8")
+    for k, s in (("x", saved.x), ("r", saved.r), ("i", saved.i)):
+        q = binding.pack8(p[k])
+        assert torch.equal(s.codes, q.codes) and torch.equal(s.exps, q.exps)
+
+
+def test_a_long_chain_and_a_single_one():
+    """Many tiles of one chain in flight at once; the bits are those of any other cut
+    of the batch into calls."""
+    p = problem((3, 20000, 64), "bf16", seed=19)
+    y, fin = binding.glr_forward(p["x"], p["r"], p["i"], p["A"], init_state=p["h0"], return_final_state=True)
+    for b in range(3):
+        yb, fb = binding.glr_forward(*(p[k][b: b + 1] for k in "xri"), p["A"], init_state=p["h0"][b: b + 1],
+                                     return_final_state=True)
+        assert torch.equal(yb[0], y[b]) and torch.equal(fb[0], fin[b])
+    cu = [0, 20000, 40000, 60000]
+    yv, fv = binding.glr_forward(*(p[k].view(1, 60000, 64) for k in "xri"), p["A"], init_state=p["h0"],
+                                 cu_seqlens=cu, return_final_state=True)
+    assert torch.equal(yv.view_as(y), y) and torch.equal(fv, fin)
+    assert binding.device_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values a tensor: the last row's bits are those of a call of its own."""
+    B, T, C = 3, 70000, 10240
+    g = torch.Generator(device=DEV)
+    g.manual_seed(21)
+    x = torch.randn(B, T, C, generator=g, device=DEV, dtype=torch.bfloat16)
+    A = -torch.exp(-5 * torch.rand(C, generator=g, device=DEV))
+    r, i = x.roll(1, 0), x.roll(1, 2)
+    y, saved = binding.glr_forward(x, r, i, A, save="packed8")
+    last = slice(B - 1, B)
+    one, kept = binding.glr_forward(x[last], r[last], i[last], A, save="packed8")
+    assert torch.equal(y[last], one)
+    assert torch.equal(saved.r.codes[last], kept.r.codes) and torch.equal(saved.r.exps[last], kept.r.exps)
+    grads = binding.glr_backward(y, saved)
+    alone = binding.glr_backward(one, kept)
+    for k in ("dx", "dr", "di"):
+        assert torch.equal(grads[k][last], alone[k])
+    q = binding.pack8(r)
+    assert torch.equal(q.codes, saved.r.codes) and torch.equal(q.exps, saved.r.exps)
+    assert torch.equal(binding.unpack8(q)[last], binding.unpack8(kept.r))

@@ -158,3 +158,23 @@ def test_same_bits_captured(oracle):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values a tensor, slices of one projection among them."""
+    b, t, g, n = 2, 140000, 32, 256
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(8)
+    rows = torch.randn(b, t, 2 * g * n, generator=gen, device=DEV, dtype=torch.bfloat16)
+    B, C = (v.unflatten(-1, (g, n)) for v in rows.split(g * n, -1))
+    pos = torch.arange(t, device=DEV).expand(b, t).contiguous()
+    freq = 10000.0 ** (-torch.arange(64, device=DEV, dtype=torch.float32) / 64)
+    Bo, Co = binding.norm_rotate(B, C, pos, freq)
+    at = slice(t - 100, t)
+    few = [v[1:, at] for v in (B, C)]
+    assert rows.numel() > 1 << 32
+    B1, C1 = binding.norm_rotate(*few, pos[1:, at].contiguous(), freq)
+    assert torch.equal(Bo[1:, at], B1) and torch.equal(Co[1:, at], C1)
+    gr = binding.norm_rotate_backward(Bo, Co, B, C, pos, freq)
+    g1 = binding.norm_rotate_backward(B1, C1, *few, pos[1:, at].contiguous(), freq)
+    assert torch.equal(gr["dB"][1:, at], g1["dB"]) and torch.equal(gr["dC"][1:, at], g1["dC"])

@@ -239,3 +239,20 @@ def test_binding_refusals_on_the_device():
     refuse(binding.norm_rotate, B, B, pos, f, weight_B=A[:4])
     refuse(binding.norm_rotate, B, B, pos, f, eps=0.0)
     refuse(binding.norm_rotate_backward, B[:, :2], B, B, B, pos, f)
+
+
+def test_ssd_backward_packed8_refusals(lib):
+    d = binding.make_dims(batch=1, seqlen=64, nheads=2, headdim=64, dstate=64, ngroups=1, dtype="bf16")
+
+    def call(pk, chunk=64, **kw):
+        p = [FAKE] * 3 + [chunk, None, FAKE, None] + [FAKE] * 6 + [None]  # dt A D | chunk h0 dy dfin | dx .. dD | dinit
+        for k, v in kw.items():
+            p[int(k[1:])] = v
+        return lib.ssd_backward_packed8(ctypes.byref(d), pk, *p, None)
+
+    assert call(None) == NULL
+    assert call(packed(codes=None)) == NULL and call(packed(last=None)) == NULL
+    assert call(packed(exps=FAKE + 1)) == MISALIGNED
+    assert call(packed(), chunk=63) == UNSUPPORTED
+    assert call(packed(), a0=None) == NULL and call(packed(), a5=None) == NULL
+    assert call(packed(), a7=FAKE + 4) == MISALIGNED

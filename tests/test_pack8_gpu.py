@@ -70,3 +70,28 @@ def test_a_large_activation_on_another_stream():
     # packing what was read back gives it again
     again = binding.unpack8(binding.pack8(got))
     assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("shape", [dict(batch=2, seqlen=200, nheads=4, headdim=64, dstate=64, ngroups=2, chunk_len=64, dtype="bf16"),
+                                   dict(batch=1, seqlen=96, nheads=3, headdim=5, dstate=7, ngroups=1, chunk_len=32, dtype="f32")],
+                         ids=["bf16", "f32"])
+def test_ssd_backward_from_checkpoints(shape):
+    """ssd_backward_packed8 is ssd_backward at the values read back, bit for bit."""
+    from structured_state_space_mamba_b200.inputs import make_inputs
+    inp = make_inputs(**shape, seed=5, init_state=True)
+    t = torch.bfloat16 if shape["dtype"] == "bf16" else torch.float32
+    dev = lambda a, ty=torch.float32: torch.from_numpy(np.ascontiguousarray(a)).to(DEV).to(ty)  # noqa: E731
+    x, B, C = dev(inp.x, t), dev(inp.B, t), dev(inp.C, t)
+    dt, A, D, h0 = dev(inp.dt), dev(inp.A), dev(inp.D), dev(inp.h0)
+    dy = torch.randn_like(x)
+    px, pB, pC = binding.pack8(x), binding.pack8(B), binding.pack8(C)
+    kw = dict(D=D, chunk_len=inp.chunk_len, init_state=h0, dfinal_state=torch.randn_like(h0))
+    got = binding.backward_packed8(px, dt, A, pB, pC, dy, **kw)
+    want = binding.backward(binding.unpack8(px, t), dt, A, binding.unpack8(pB, t), binding.unpack8(pC, t), dy, **kw)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    for bad in (dict(x=x), dict(B=pC.codes), dict(dy=dy[:, :5]), dict(dt=dt.double())):
+        a = dict(x=px, dt=dt, A=A, B=pB, C=pC, dy=dy)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            binding.backward_packed8(**a, **kw)
