@@ -2,8 +2,8 @@
 // format).
 //
 // HBM-bound: a value is 2 or 4 bytes read and 1 + 1/64 written, or the reverse.
-// Eight lanes take a block of 64 values, 16 or 32 bytes a lane in one or two
-// vectors, and find its largest magnitude by shuffles; a thread has kUnroll
+// Eight (bf16) or sixteen (fp32) lanes take a block of 64 values, one 16-byte vector
+// a lane, and find its largest magnitude by shuffles; a thread has kUnroll
 // blocks' loads in flight.  Rows that are no whole number of 8-value vectors go
 // a warp a block with single-value accesses, eight blocks in flight.
 #include "common.cuh"
@@ -17,7 +17,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+// values of a lane: one 16-byte vector
+template <typename T> constexpr int kVals = 16 / sizeof(T);
+
+__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&v)[8]) {
     const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -26,12 +29,11 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+__device__ __forceinline__ void load_vec(const float *p, float (&v)[4]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -40,16 +42,23 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+// the codes of a lane's values
+__device__ __forceinline__ void store_codes(int8_t *p, const float (&v)[8], uint32_t ex) {
+    *reinterpret_cast<uint2 *>(p) = pack8_eight(v, ex);
+}
+__device__ __forceinline__ void store_codes(int8_t *p, const float (&v)[4], uint32_t ex) {
+    *reinterpret_cast<uint32_t *>(p) = pack8_four(v, ex);
 }
 
-// Where a lane's eight values of its blocks lie: the first by a division, the next
-// ones, kThreads / 8 blocks on, by steps of whole rows and blocks of a row.  FLAT:
-// whole blocks only, rows follow each other.
-template <bool FLAT>
+// Where a lane's VALS values of its blocks lie: the first by a division, the next
+// ones, kPer blocks on, by steps of whole rows and blocks of a row.  FLAT: whole
+// blocks only, rows follow each other.
+template <bool FLAT, int VALS>
 struct Place {
+    static constexpr int kLanes = kPackBlock / VALS, kPer = kThreads / kLanes;
     int64_t row, c, rows_on, blocks_on, nb, cols;
     int sub;
     __device__ __forceinline__ Place(int64_t n, int64_t nb_, int64_t cols_, int sub_)
@@ -59,23 +68,23 @@ struct Place {
         } else {
             row = n / nb;
             c = n - row * nb;
-            rows_on = (kThreads / 8) / nb;
-            blocks_on = (kThreads / 8) - rows_on * nb;
+            rows_on = kPer / nb;
+            blocks_on = kPer - rows_on * nb;
         }
     }
     // the place; false behind the row's end
     __device__ __forceinline__ bool at(int64_t &o) const {
         if (FLAT) {
-            o = row * kPackBlock + sub * 8;
+            o = row * kPackBlock + sub * VALS;
             return true;
         }
-        const int64_t v = c * kPackBlock + sub * 8;
+        const int64_t v = c * kPackBlock + sub * VALS;
         o = row * cols + v;
         return v < cols;
     }
     __device__ __forceinline__ void on() {
         if (FLAT) {
-            row += kThreads / 8;
+            row += kPer;
         } else {
             row += rows_on;
             c += blocks_on;
@@ -91,32 +100,34 @@ template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kThreads)
 pack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const T *__restrict__ x, int8_t *__restrict__ codes,
              uint8_t *__restrict__ exps) {
-    constexpr int kPer = kThreads / 8;  // blocks of one step
-    const int sub = threadIdx.x & 7;
-    const int64_t n0 = int64_t(blockIdx.x) * kPer * kUnroll + (threadIdx.x >> 3);
-    float v[kUnroll][8];
+    constexpr int V = kVals<T>;
+    using P = Place<FLAT, V>;
+    constexpr int kPer = P::kPer;  // blocks of one step
+    const int sub = threadIdx.x % P::kLanes;
+    const int64_t n0 = int64_t(blockIdx.x) * kPer * kUnroll + threadIdx.x / P::kLanes;
+    float v[kUnroll][V];
     int64_t o[kUnroll];
     bool ok[kUnroll];
-    Place<FLAT> place(n0, nb, cols, sub);
+    P place(n0, nb, cols, sub);
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k, place.on()) {
         const int64_t n = n0 + k * kPer;
         ok[k] = place.at(o[k]) && n < blocks;
-        if (ok[k]) load8(x + o[k], v[k]);
+        if (ok[k]) load_vec(x + o[k], v[k]);
         else
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[k][e] = 0.f;
+            for (int e = 0; e < V; ++e) v[k][e] = 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
         uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[k][e]) & 0x7fffffffu);
+        for (int e = 0; e < V; ++e) m = max(m, __float_as_uint(v[k][e]) & 0x7fffffffu);
 #pragma unroll
-        for (int s = 4; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+        for (int s = P::kLanes / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
         if (!ok[k]) continue;
         const uint32_t ex = pack8_exp(m);
-        *reinterpret_cast<uint2 *>(codes + o[k]) = pack8_eight(v[k], ex);
+        store_codes(codes + o[k], v[k], ex);
         if (sub == 0) exps[n0 + k * kPer] = uint8_t(ex);
     }
 }
@@ -125,34 +136,41 @@ template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kThreads)
 unpack8_kernel(int64_t blocks, int64_t nb, int64_t cols, const int8_t *__restrict__ codes,
                const uint8_t *__restrict__ exps, T *__restrict__ out) {
-    constexpr int kPer = kThreads / 8;
-    const int sub = threadIdx.x & 7;
-    const int64_t n0 = int64_t(blockIdx.x) * kPer * kUnroll + (threadIdx.x >> 3);
-    uint2 q[kUnroll];
-    uint32_t ex[kUnroll];
+    constexpr int V = kVals<T>;
+    using P = Place<FLAT, V>;
+    constexpr int kPer = P::kPer;
+    const int sub = threadIdx.x % P::kLanes;
+    const int64_t n0 = int64_t(blockIdx.x) * kPer * kUnroll + threadIdx.x / P::kLanes;
+    uint32_t q[kUnroll][V / 4], ex[kUnroll];
     int64_t o[kUnroll];
     bool ok[kUnroll];
-    Place<FLAT> place(n0, nb, cols, sub);
+    P place(n0, nb, cols, sub);
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k, place.on()) {
         const int64_t n = n0 + k * kPer;
         ok[k] = place.at(o[k]) && n < blocks;
         if (!ok[k]) continue;
-        q[k] = __ldg(reinterpret_cast<const uint2 *>(codes + o[k]));
+        if constexpr (V == 8) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(codes + o[k]));
+            q[k][0] = w.x;
+            q[k][1] = w.y;
+        } else {
+            q[k][0] = __ldg(reinterpret_cast<const uint32_t *>(codes + o[k]));
+        }
         ex[k] = __ldg(exps + n);
     }
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
         if (!ok[k]) continue;
         const float step = pack8_step(ex[k]);
-        float v[8];
+        float v[V];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const float2 two = unpack8_two((e < 4 ? q[k].x : q[k].y) >> (8 * (e & 2)), step);
+        for (int e = 0; e < V; e += 2) {
+            const float2 two = unpack8_two(q[k][e / 4] >> (8 * (e & 2)), step);
             v[e] = two.x;
             v[e + 1] = two.y;
         }
-        store8(out + o[k], v);
+        store_vec(out + o[k], v);
     }
 }
 
@@ -188,8 +206,11 @@ pack8_any_kernel(int64_t blocks, int64_t nb, int64_t cols, const T *__restrict__
         const uint32_t ex = pack8_exp(__reduce_max_sync(
             0xffffffffu, max(__float_as_uint(v[k][0]) & 0x7fffffffu, __float_as_uint(v[k][1]) & 0x7fffffffu)));
         const float inv = pack8_inv(ex);
-        if (lane < left[k]) codes[o[k]] = int8_t(pack8_code(v[k][0], inv));
-        if (lane + 32 < left[k]) codes[o[k] + 32] = int8_t(pack8_code(v[k][1], inv));
+        const bool edge = ex >= kPackEdge;  // the same for the whole warp
+        const uint32_t a = edge ? uint32_t(pack8_code(v[k][0], inv)) : pack8_fast(v[k][0], inv);
+        const uint32_t b = edge ? uint32_t(pack8_code(v[k][1], inv)) : pack8_fast(v[k][1], inv);
+        if (lane < left[k]) codes[o[k]] = int8_t(a);
+        if (lane + 32 < left[k]) codes[o[k] + 32] = int8_t(b);
         if (lane == 0) exps[n0 + k] = uint8_t(ex);
     }
 }
@@ -231,11 +252,12 @@ struct Plan {
     unsigned vec_grid, any_grid;
     bool fits;
 };
+template <typename T>
 Plan plan_of(int64_t rows, int64_t cols) {
     Plan p;
     p.nb = (cols + kPackBlock - 1) / kPackBlock;
     p.blocks = rows * p.nb;
-    const int64_t per = kThreads / 8 * kUnroll, any = kThreads / 32 * kRun;
+    const int64_t per = Place<true, kVals<T>>::kPer * kUnroll, any = kThreads / 32 * kRun;
     const int64_t g = (p.blocks + per - 1) / per, h = (p.blocks + any - 1) / any;
     p.fits = g <= 0x7fffffff && h <= 0x7fffffff;
     p.vec_grid = unsigned(g);
@@ -245,11 +267,11 @@ Plan plan_of(int64_t rows, int64_t cols) {
 
 template <typename T>
 cudaError_t pack_typed(int64_t rows, int64_t cols, const T *x, int8_t *codes, uint8_t *exps, cudaStream_t st) {
-    const Plan p = plan_of(rows, cols);
+    const Plan p = plan_of<T>(rows, cols);
     if (!p.fits) return cudaErrorInvalidValue;
     if (cols % kPackBlock == 0)
         pack8_kernel<T, true><<<p.vec_grid, kThreads, 0, st>>>(p.blocks, p.nb, cols, x, codes, exps);
-    else if (cols % 8 == 0)
+    else if (cols % kVals<T> == 0)
         pack8_kernel<T, false><<<p.vec_grid, kThreads, 0, st>>>(p.blocks, p.nb, cols, x, codes, exps);
     else
         pack8_any_kernel<T><<<p.any_grid, kThreads, 0, st>>>(p.blocks, p.nb, cols, x, codes, exps);
@@ -258,11 +280,11 @@ cudaError_t pack_typed(int64_t rows, int64_t cols, const T *x, int8_t *codes, ui
 template <typename T>
 cudaError_t unpack_typed(int64_t rows, int64_t cols, const int8_t *codes, const uint8_t *exps, T *out,
                          cudaStream_t st) {
-    const Plan p = plan_of(rows, cols);
+    const Plan p = plan_of<T>(rows, cols);
     if (!p.fits) return cudaErrorInvalidValue;
     if (cols % kPackBlock == 0)
         unpack8_kernel<T, true><<<p.vec_grid, kThreads, 0, st>>>(p.blocks, p.nb, cols, codes, exps, out);
-    else if (cols % 8 == 0)
+    else if (cols % kVals<T> == 0)
         unpack8_kernel<T, false><<<p.vec_grid, kThreads, 0, st>>>(p.blocks, p.nb, cols, codes, exps, out);
     else
         unpack8_any_kernel<T><<<p.any_grid, kThreads, 0, st>>>(p.blocks, p.nb, cols, codes, exps, out);

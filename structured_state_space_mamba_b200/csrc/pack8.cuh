@@ -47,19 +47,19 @@ __device__ __forceinline__ int pack8_code(float v, float inv) {
 __device__ __forceinline__ uint32_t pack8_fast(float v, float inv) {
     return __float_as_uint(fmaf(v, inv, 12582912.f));
 }
-// Eight values of a block as codes.
-__device__ __forceinline__ uint2 pack8_eight(const float (&v)[8], uint32_t ex) {
+// Four, and eight, values of a block as codes.
+__device__ __forceinline__ uint32_t pack8_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t pack8_four(const float (&v)[4], uint32_t ex) {
     const float inv = pack8_inv(ex);
-    uint32_t q[8];
-    if (ex < kPackEdge) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = pack8_fast(v[e], inv);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = uint32_t(pack8_code(v[e], inv));
-    }
-    return make_uint2(__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
-                      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+    if (ex < kPackEdge)
+        return pack8_bytes(pack8_fast(v[0], inv), pack8_fast(v[1], inv), pack8_fast(v[2], inv), pack8_fast(v[3], inv));
+    return pack8_bytes(pack8_code(v[0], inv), pack8_code(v[1], inv), pack8_code(v[2], inv), pack8_code(v[3], inv));
+}
+__device__ __forceinline__ uint2 pack8_eight(const float (&v)[8], uint32_t ex) {
+    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+    return make_uint2(pack8_four(lo, ex), pack8_four(hi, ex));
 }
 // Two codes (the low bytes of a word) as numbers: a byte with its sign bit flipped,
 // in the mantissa of 2^23, is 8388736 + code.  Without conversions for the same
