@@ -64,32 +64,40 @@ __device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a,
 __device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// Operations with a constant stay scalar: there it is an immediate, while a packed
-// operation needs it in a pair of registers (moving those there cost a quarter
-// of all instructions).
-__device__ __forceinline__ float2 scale(float2 a, float c) { return make_float2(a.x * c, a.y * c); }
+// Operations with a constant are scalar: there it is an immediate, while a packed
+// operation needs it in a pair of registers, and moving those there cost a
+// quarter of all instructions.  The two constants of the sigmoids are worth
+// their registers; an assignment that the compiler cannot see through keeps them.
 __device__ __forceinline__ float2 plus(float2 a, float c) { return make_float2(a.x + c, a.y + c); }
 __device__ __forceinline__ float2 times_plus(float2 a, float2 b, float c) {
     return make_float2(fmaf(a.x, b.x, c), fmaf(a.y, b.y, c));
 }
 constexpr float kLog2e = 1.4426950408889634f;
+struct Held {
+    float2 one, k;  // 1 and -log2(e)
+    __device__ __forceinline__ Held() : one(both(1.f)), k(both(-kLog2e)) {
+        asm volatile("" : "+f"(one.x), "+f"(one.y), "+f"(k.x), "+f"(k.y));
+    }
+};
 
-// e^-v (v held at -43 from below), and s(v) from it; 1 - s(v) = e^-v s(v)
-__device__ __forceinline__ float2 decayed(float2 v) {
-    return make_float2(ex2(max_nan(v.x, -43.f) * -kLog2e), ex2(max_nan(v.y, -43.f) * -kLog2e));
+// The argument of a sigmoid: at least -43 (s(-43) = 2e-19), NaN as it is.
+__device__ __forceinline__ float2 at_least(float2 v) { return make_float2(max_nan(v.x, -43.f), max_nan(v.y, -43.f)); }
+// e^-v, and s(v) from it; 1 - s(v) = e^-v s(v)
+__device__ __forceinline__ float2 decayed(const Held &hd, float2 v) {
+    const float2 t = mul(v, hd.k);
+    return make_float2(ex2(t.x), ex2(t.y));
 }
-__device__ __forceinline__ float2 sigmoid(float2 e) {
-    const float2 d = plus(e, 1.f);
-    return make_float2(rcp(d.x), rcp(d.y));
-}
-// The two sigmoids by one reciprocal: with the arguments held at -43 the product of
-// the denominators stays finite (s(-43) = 2e-19).
+// The two sigmoids of arguments from -43 on by one reciprocal: the product of the
+// denominators stays finite.
 struct Sig {
     float2 sr, si;  // s(r), s(i)
+    float2 er, ei;  // e^-r, e^-i: 1 - s(r) = er * sr
 };
-__device__ __forceinline__ Sig sigmoids(float2 r, float2 i) {
+__device__ __forceinline__ Sig sigmoids(const Held &hd, float2 r, float2 i) {
     Sig g;
-    const float2 dr = plus(decayed(r), 1.f), di = plus(decayed(i), 1.f);
+    g.er = decayed(hd, r);
+    g.ei = decayed(hd, i);
+    const float2 dr = add(g.er, hd.one), di = add(g.ei, hd.one);
     const float2 d = mul(dr, di), q = make_float2(rcp(d.x), rcp(d.y));
     g.sr = mul(di, q);
     g.si = mul(dr, q);
@@ -99,14 +107,14 @@ __device__ __forceinline__ Sig sigmoids(float2 r, float2 i) {
 __device__ __forceinline__ bool steep_warp(float2 A) {
     return __any_sync(0xffffffffu, A.x < -0.5f || A.y < -0.5f);
 }
-// e^l - 1 for l <= 0: the Taylor sum to l^7 from -1/2 up (the next term is below
-// 2^-22 of the result there), the exponential below (where its error is no
-// longer magnified by the difference).
+// e^l - 1 for l <= 0.  From -1/2 up, l + l^2 q(l) with q the polynomial of degree 4
+// that meets (e^l - 1 - l) / l^2 at the five Chebyshev nodes of [-1/2, 0]: 1.3e-8
+// of the result off, at most.  Below, the exponential, whose error the
+// difference no longer magnifies.
 __device__ __forceinline__ float2 decay_minus_1(float2 l, bool steep) {
-    float2 p = make_float2(fmaf(l.x, 1.f / 5040.f, 1.f / 720.f), fmaf(l.y, 1.f / 5040.f, 1.f / 720.f));
-    p = times_plus(l, p, 1.f / 120.f);
-    p = times_plus(l, p, 1.f / 24.f);
-    p = times_plus(l, p, 1.f / 6.f);
+    float2 p = make_float2(fmaf(l.x, 0.0011642870f, 0.0082382215f), fmaf(l.y, 0.0011642870f, 0.0082382215f));
+    p = times_plus(l, p, 0.0416499302f);
+    p = times_plus(l, p, 0.1666656286f);
     p = times_plus(l, p, 0.5f);
     p = fma(mul(l, p), l, l);
     if (steep) {
@@ -117,9 +125,10 @@ __device__ __forceinline__ float2 decay_minus_1(float2 l, bool steep) {
 }
 // a^2 - 1 from a - 1
 __device__ __forceinline__ float2 square_minus_1(float2 e1) { return fma(e1, e1, add(e1, e1)); }
-// decay - 1 and what the token brings in, sqrt(1 - a^2) s(i) x
-__device__ __forceinline__ void token(float2 x, float2 r, float2 i, float2 A, bool steep, float2 &e1, float2 &u) {
-    const Sig g = sigmoids(r, i);
+// decay - 1 and what the token brings in, sqrt(1 - a^2) s(i) x, for r and i from -43 on
+__device__ __forceinline__ void token(const Held &hd, float2 x, float2 r, float2 i, float2 A, bool steep, float2 &e1,
+                                      float2 &u) {
+    const Sig g = sigmoids(hd, r, i);
     e1 = decay_minus_1(mul(A, g.sr), steep);
     const float2 w = square_minus_1(e1);
     u = mul(make_float2(root(-w.x), root(-w.y)), mul(g.si, x));
@@ -141,6 +150,17 @@ __device__ __forceinline__ float2 unpack2(const T *p) {
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     } else {
         return *reinterpret_cast<const float2 *>(p);
+    }
+}
+// the same, at least -43: in 16 bits before they are widened
+template <typename T>
+__device__ __forceinline__ float2 unpack2_at_least(const T *p) {
+    if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(p), __float2bfloat162_rn(-43.f));
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&v);
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+        return at_least(unpack2(p));
     }
 }
 template <bool VEC>
@@ -611,6 +631,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         const int c = t.ct * kGlrCols + 2 * lane;
         return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
+    const Held hd;
     for (int k = 0; k < NS; ++k) load(k);
     float2 A = rates(0);
     for (int k = 0;; ++k) {
@@ -652,7 +673,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
             const int o = j * kGlrCols + 2 * lane;
-            token(unpack2(st.x + o), unpack2(st.r + o), unpack2(st.i + o), A, steep, e1[j], u[j]);
+            token(hd, unpack2(st.x + o), unpack2_at_least(st.r + o), unpack2_at_least(st.i + o), A, steep, e1[j], u[j]);
         }
         if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
@@ -854,6 +875,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         const int c = t.ct * kGlrCols + 2 * lane;
         return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
+    const Held hd;
     for (int k = 0; k < NS; ++k) load(k);
     float2 A = rates(0);
     int k = 0;
@@ -882,12 +904,16 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 return unpack2(st.in[n] + o);
             }
         };
+        auto gate = [&](int n, int j) -> float2 {  // r or i, at least -43
+            if constexpr (PACK) return at_least(input(n, j));
+            else return unpack2_at_least(st.in[n] + j * kGlrCols + 2 * lane);
+        };
         auto cotangent = [&](int j) -> float2 { return unpack2(st.dy + j * kGlrCols + 2 * lane); };
         float2 e1[kTok], u[kTok];
         {
             float2 P = both(1.f), S = both(0.f), R = both(0.f);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) token(input(0, j), input(1, j), input(2, j), A, steep, e1[j], u[j]);
+            for (int j = 0; j < kTok; ++j) token(hd, input(0, j), gate(1, j), gate(2, j), A, steep, e1[j], u[j]);
             if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
                 for (int j = 0; j < kTok; ++j)
@@ -927,9 +953,8 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
 #pragma unroll
             for (int j = kTok - 1; j >= 0; --j, o -= C) {
                 if (!all && j >= ntok) continue;
-                const float2 er = decayed(input(1, j)), ei = decayed(input(2, j));
-                const float2 dr = plus(er, 1.f), di = plus(ei, 1.f), d = mul(dr, di);
-                const float2 q = make_float2(rcp(d.x), rcp(d.y)), sr = mul(di, q), si = mul(dr, q);
+                const Sig sg = sigmoids(hd, gate(1, j), gate(2, j));
+                const float2 sr = sg.sr, si = sg.si, er = sg.er, ei = sg.ei;
                 const float2 w = square_minus_1(e1[j]), rs = make_float2(inv_root(w.x), inv_root(w.y));
                 const float2 m = mul(make_float2(-w.x, -w.y), rs), a = plus(e1[j], 1.f), six = mul(si, input(0, j));
                 const float2 G = add(K, cotangent(j)), Gm = mul(G, m);
@@ -992,6 +1017,7 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
     const bool a0 = c < C, a1 = c + 1 < C;
     if (!a0) return;
     const float2 Av = load2<VEC>(A + c, a0, a1);
+    const Held hd;
     for (int b = blockIdx.y; b < batch; b += gridDim.y) {
         const int64_t o = int64_t(b) * C + c;
         float2 xv, rv, iv, h;
@@ -1006,7 +1032,7 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
             h = make_float2(state[o], state[n]);
         }
         float2 e1, u;
-        token(xv, rv, iv, Av, true, e1, u);
+        token(hd, xv, at_least(rv), at_least(iv), Av, true, e1, u);
         h = advance(h, e1, u);
         store2<float, VEC>(state + o, h, a0, a1);
         store2<T, VEC>(y + o, h, a0, a1);
