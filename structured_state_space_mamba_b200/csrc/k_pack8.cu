@@ -1,11 +1,13 @@
 // k_pack8.cu -- activations to 8-bit checkpoints and back (pack8.cuh has the
 // format).
 //
-// HBM-bound: a value is 2 or 4 bytes read and 1 + 1/64 written, or the reverse.
+// HBM-bound: a value is 2 or 4 bytes read and 1 + 1/64 written, or the reverse
+// (16384 x 5120: bf16 41 us to pack, 6.2 TB/s, 39 us to read back; fp32 60 and 64 us).
 // Eight (bf16) or sixteen (fp32) lanes take a block of 64 values, one 16-byte vector
 // a lane, and find its largest magnitude by shuffles; a thread has kUnroll
 // blocks' loads in flight.  Rows that are no whole number of 8-value vectors go
-// a warp a block with single-value accesses, eight blocks in flight.
+// a warp a block with single-value accesses, eight blocks in flight (20000 x 1001
+// bf16: 34 us, 1.8 TB/s).
 #include "common.cuh"
 #include "glr.h"
 #include "pack8.cuh"

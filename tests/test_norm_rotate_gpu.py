@@ -57,7 +57,8 @@ def problem(b, t, g, n, rotary, dtype, seed=0, layout="own", far=False):
 CASES = [(1, 1, 1, 128, 128, "own"), (2, 33, 3, 64, 32, 8), (1, 100, 2, 96, 64, "own"), (3, 5, 1, 256, 256, 16),
          (1, 7, 5, 8, 8, "own"), (2, 9, 2, 40, 0, 4), (1, 50, 2, 24, 12, "own"), (1, 5, 1, 1, 0, "own"),
          (2, 11, 3, 7, 6, "own"), (1, 20, 2, 128, 128, 1), (1, 3, 2, 250, 250, 3), (64, 1, 8, 128, 64, "own"),
-         (1, 3000, 1, 16, 16, "own"), (2, 3, 2, 200, 2, "own")]
+         (1, 3000, 1, 16, 16, "own"), (2, 3, 2, 200, 2, "own"), (1, 9, 2, 64, 36, "own"), (2, 7, 3, 256, 4, 8),
+         (1, 30, 2, 128, 64, 2), (1, 6, 5, 40, 20, 6)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
