@@ -181,8 +181,8 @@ __device__ __forceinline__ float2 load2(const float *p, bool a0, bool a1) {
     return make_float2(a0 ? p[0] : 0.f, a1 ? p[1] : 0.f);
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store2(T *p, float2 v, bool a0, bool a1) {
-    if (VEC) {
+__device__ __forceinline__ void store2(T *p, float2 v, bool a0, bool a1, bool even = false) {
+    if (VEC || even) {
         if (a0) {
             if constexpr (sizeof(T) == 2)
                 *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
@@ -462,6 +462,26 @@ __device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N
 #pragma unroll
             for (int a = 0; a < N; ++a) copy_async<4>(dst[a] + id, src[a] + o, ok ? 4 : 0);
         }
+    } else if (sizeof(T) == 2 && C % 2 == 0) {  // and so are rows of an even length in 16 bits
+        const bool in = c0 + 2 * lane < C;
+        int64_t o = t.base + (int64_t(warp * kTok) * C + 2 * lane);
+#pragma unroll
+        for (int n = 0; n < kTok; ++n, o += C) {
+            const bool ok = in && n < ntok;
+#pragma unroll
+            for (int a = 0; a < N; ++a)
+                copy_async<4>(dst[a] + n * kGlrCols + 2 * lane, src[a] + (ok ? o : 0), ok ? 4 : 0);
+        }
+    } else if (sizeof(T) == 1 && C % 4 == 0) {
+        const int row = lane / 16, v = lane % 16 * 4;
+        int64_t o = t.base + (int64_t(warp * kTok + row) * C + v);
+#pragma unroll
+        for (int n = 0; n < kTok; n += 2, o += 2 * int64_t(C)) {
+            const bool ok = c0 + v < C && row + n < ntok;
+#pragma unroll
+            for (int a = 0; a < N; ++a)
+                copy_async<4>(dst[a] + (n + row) * kGlrCols + v, src[a] + (ok ? o : 0), ok ? 4 : 0);
+        }
     } else {
         // single values, all of a tensor's on their way before the first is stored
 #pragma unroll
@@ -702,20 +722,21 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         load(k + NS);
         A = rates(k + 1);
         T *y = p.y + (t.base + (int64_t(warp * kTok) * C + 2 * lane));
+        const bool even = C % 2 == 0;
         tc::mbar_wait(&sync.ready, k & 1, p.err);
         float2 h = *reinterpret_cast<const float2 *>(&sm.part[warp][lane]);
         if (t.full) {
 #pragma unroll
             for (int j = 0; j < kTok; ++j, y += C) {
                 h = advance(h, e1[j], u[j]);
-                store2<T, VEC>(y, h, true, true);
+                store2<T, VEC>(y, h, true, true, even);
             }
         } else {
             const int c = t.ct * kGlrCols + 2 * lane;
 #pragma unroll
             for (int j = 0; j < kTok; ++j, y += C) {
                 h = advance(h, e1[j], u[j]);
-                if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C);
+                if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C, even);
             }
         }
     }
@@ -960,7 +981,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         }
         int64_t o = t.base + (int64_t(warp * kTok + kTok - 1) * C + 2 * lane);
         const int c = t.ct * kGlrCols + 2 * lane;
-        const bool a0 = c < C, a1 = c + 1 < C;
+        const bool a0 = c < C, a1 = c + 1 < C, even = C % 2 == 0;
         auto walk = [&](bool all) {
 #pragma unroll
             for (int j = kTok - 1; j >= 0; --j, o -= C) {
@@ -976,9 +997,9 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 const float2 dl = mul(mul(G, a), add(u[j], make_float2(-as.x, -as.y)));
                 dA = fma(dl, sr, dA);
                 K = fma(e1[j], G, G);
-                store2<T, VEC>(p.dx + o, mul(Gm, si), all || a0, all || a1);
-                store2<T, VEC>(p.di + o, mul(mul(Gm, six), mul(ei, si)), all || a0, all || a1);
-                store2<T, VEC>(p.dr + o, mul(mul(dl, mul(A, sr)), mul(er, sr)), all || a0, all || a1);
+                store2<T, VEC>(p.dx + o, mul(Gm, si), all || a0, all || a1, even);
+                store2<T, VEC>(p.di + o, mul(mul(Gm, six), mul(ei, si)), all || a0, all || a1, even);
+                store2<T, VEC>(p.dr + o, mul(mul(dl, mul(A, sr)), mul(er, sr)), all || a0, all || a1, even);
             }
         };
         if (t.full) walk(true);
