@@ -362,7 +362,11 @@ SSD_API ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const f
  * fewer than 2^31 tiles of 64 channels and SSD_GLR_CHUNK tokens (else
  * SSD_ERR_UNSUPPORTED); dtype is the storage type of x, r, i, y and their
  * gradients, A, states and dA are fp32.  States and sums are held in fp32;
- * every pass gives the same bits for the same inputs.
+ * every pass gives the same bits for the same inputs, however a batch is cut
+ * into calls.  Gates saturate at s(-43) = 2e-19.  A NaN or an infinity stays in
+ * its channel of its sequence: before its token nothing changes, from it on the
+ * states are NaN or infinite.  Tiles of one call wait for each other on the device,
+ * with a limit (ssd_device_status).
  */
 typedef struct {
     int64_t batch;    /* B */
@@ -481,8 +485,8 @@ SSD_API ssd_status_t ssd_glr_backward(const ssd_glr_dims_t *dims, const int64_t 
 /*
  * ssd_glr_step -- one token of the recurrence for every row: the decode step
  * on a resident state.  dims->seqlen must be 1; x_t, r_t, i_t, y_t [B, C]
- * dtype; state [B, C] fp32, read and overwritten with the new state.  One
- * launch, no allocation.
+ * dtype; state [B, C] fp32, read and overwritten with the new state; y_t must
+ * not alias the inputs or the state.  One launch, no allocation.
  */
 SSD_API ssd_status_t ssd_glr_step(const ssd_glr_dims_t *dims, const void *x_t, const void *r_t, const void *i_t,
                                   const float *A, float *state, void *y_t, void *stream);
@@ -510,8 +514,8 @@ SSD_API ssd_status_t ssd_glr_step(const ssd_glr_dims_t *dims, const void *x_t, c
  *   B_out, C_out  [B, T, G, N] dtype, contiguous; must not alias the inputs
  * 1 <= dstate <= 256, rotary even and 0 <= rotary <= dstate, eps > 0 (else
  * SSD_ERR_INVALID_DIM, or SSD_ERR_UNSUPPORTED for dstate > 256 or
- * batch * seqlen >= 2^31).  Pointers into Bm and Cm need the alignment of their
- * element type only.  One launch.
+ * batch * seqlen >= 2^31, ngroups > 2^20).  Bm, Cm, positions, inv_freq and the
+ * weights need the alignment of their elements only.  One launch.
  */
 typedef struct {
     int64_t batch, seqlen, ngroups, dstate;

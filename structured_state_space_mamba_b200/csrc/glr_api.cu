@@ -162,8 +162,12 @@ ssd_status_t rotate_shape(const ssd_rotate_dims_t *dims, ssd::RotateShape *s) {
     return SSD_OK;
 }
 
-bool unaligned_element(const void *p, int dtype) {
-    return (reinterpret_cast<uintptr_t>(p) & (dtype == SSD_BF16 ? 1u : 3u)) != 0;
+bool off(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+// what a norm and rotation reads: whole tensors on 16 bytes, the rest by elements
+bool off_rotate(const ssd_rotate_dims_t &a, const void *Bm, const void *Cm, const int64_t *positions,
+                const float *inv_freq, const float *weight_B, const float *weight_C) {
+    const uintptr_t es = a.dtype == SSD_BF16 ? 2 : 4;
+    return off(Bm, es) || off(Cm, es) || off(positions, 8) || off(inv_freq, 4) || off(weight_B, 4) || off(weight_C, 4);
 }
 
 }  // namespace
@@ -308,10 +312,9 @@ ssd_status_t ssd_norm_rotate(const ssd_rotate_dims_t *dims, const void *Bm, cons
     const ssd_status_t s = rotate_shape(dims, &sh);
     if (s != SSD_OK) return s;
     if (!Bm || !Cm || !positions || (!inv_freq && sh.rotary) || !B_out || !C_out) return SSD_ERR_NULL_ARG;
-    const void *ptrs[] = {positions, inv_freq, weight_B, weight_C, B_out, C_out};
-    for (const void *p : ptrs)
-        if (misaligned(p)) return SSD_ERR_MISALIGNED;
-    if (unaligned_element(Bm, dims->dtype) || unaligned_element(Cm, dims->dtype)) return SSD_ERR_MISALIGNED;
+    if (misaligned(B_out) || misaligned(C_out) ||
+        off_rotate(*dims, Bm, Cm, positions, inv_freq, weight_B, weight_C))
+        return SSD_ERR_MISALIGNED;
     return ssd::launch_norm_rotate(sh, dims->dtype == SSD_BF16, Bm, Cm, positions, inv_freq, weight_B, weight_C,
                                    B_out, C_out, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? SSD_OK
@@ -327,10 +330,11 @@ ssd_status_t ssd_norm_rotate_backward(const ssd_rotate_dims_t *dims, const void 
     if (s != SSD_OK) return s;
     if (!dB_out || !dC_out || !Bm || !Cm || !positions || (!inv_freq && sh.rotary) || !dB || !dC)
         return SSD_ERR_NULL_ARG;
-    const void *ptrs[] = {dB_out, dC_out, positions, inv_freq, weight_B, weight_C, dB, dC, dweight_B, dweight_C};
+    const void *ptrs[] = {dB_out, dC_out, dB, dC};
     for (const void *p : ptrs)
         if (misaligned(p)) return SSD_ERR_MISALIGNED;
-    if (unaligned_element(Bm, dims->dtype) || unaligned_element(Cm, dims->dtype)) return SSD_ERR_MISALIGNED;
+    if (off_rotate(*dims, Bm, Cm, positions, inv_freq, weight_B, weight_C) || off(dweight_B, 4) || off(dweight_C, 4))
+        return SSD_ERR_MISALIGNED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     float *part = nullptr;
     if (dweight_B || dweight_C) {

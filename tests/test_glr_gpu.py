@@ -299,6 +299,30 @@ def test_checkpoints_of_values_at_the_edge(dtype, C):
         assert torch.equal(s.codes, q.codes) and torch.equal(s.exps, q.exps)
 
 
+def test_any_bits_of_a_nan():
+    """A NaN of all ones, the bits that mark what is not written yet between tiles,
+    in the inputs and in the states given: it comes out as a NaN, and nothing waits for it."""
+    p = problem((1, 400, 70), "f32", seed=18)
+    ones = torch.tensor([-1], dtype=torch.int32, device=DEV).view(torch.float32)
+    p["x"][0, 100, 3], p["r"][0, 150, 4], p["i"][0, 64, 5] = ones, ones, ones
+    p["h0"][0, 6], p["dfin"][0, 7], p["dy"][0, 200, 8] = ones, ones, ones
+    y, fin, saved = binding.glr_forward(p["x"], p["r"], p["i"], p["A"], init_state=p["h0"], return_final_state=True,
+                                        save="inputs")
+    g = binding.glr_backward(p["dy"], saved, dfinal_state=p["dfin"], return_dinit_state=True)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    first = {3: 100, 4: 150, 5: 64, 6: 0}
+    for c in range(70):
+        t = first.get(c, 400)
+        assert torch.isnan(y[0, t:, c]).all() and torch.isfinite(y[0, :t, c]).all(), c
+    assert torch.isnan(fin[0, list(first)]).all()
+    # backwards from the cotangents' NaN to the start (and through a gate that is one)
+    assert torch.isnan(g["dx"][0, :, 7]).all() and torch.isnan(g["dx"][0, :201, 8]).all()
+    assert torch.isfinite(g["dx"][0, 201:, 8]).all() and torch.isnan(g["dinit_state"][0, [4, 7, 8]]).all()
+    quiet = [c for c in range(70) if c not in (3, 4, 5, 6, 7, 8)]
+    assert all(torch.isfinite(g[k][..., quiet]).all() for k in ("dx", "dr", "di", "dA"))
+
+
 def test_a_long_chain_and_a_single_one():
     """Many tiles of one chain in flight at once; the bits are those of any other cut
     of the batch into calls."""
