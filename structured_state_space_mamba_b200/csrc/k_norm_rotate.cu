@@ -331,25 +331,33 @@ norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__re
         Turn<T, INTER> turn;
         turn.at(act ? double(__ldg(positions + tok)) : 0.0, freq);
         int64_t o = tok * s.G * s.N;
-        for (int g = 0; g < s.G; ++g, o += s.N, xb += s.N, xc += s.N) {
-            typename Raw<T>::type raw[8] = {};
-            if (act) {
-                fetch_lane<WIDE>(xb, l, raw[0], raw[1]);
-                fetch_lane<WIDE>(dBo + o, l, raw[2], raw[3]);
-                fetch_lane<WIDE>(xc, l, raw[4], raw[5]);
-                fetch_lane<WIDE>(dCo + o, l, raw[6], raw[7]);
-            }
+        // while B's row is worked on C's is on its way, and the other way round
+        typename Raw<T>::type rb[4] = {}, rc[4] = {};
+        auto fetch = [&](const T *x, const T *d, typename Raw<T>::type (&r)[4]) {
+            fetch_lane<WIDE>(x, l, r[0], r[1]);
+            fetch_lane<WIDE>(d, l, r[2], r[3]);
+        };
+        auto row = [&](const typename Raw<T>::type (&r)[4], float2 (&x)[4], float2 (&d)[4]) {
+            widen4(r[0], x);
+            widen4(r[1], x + 2);
+            widen4(r[2], d);
+            widen4(r[3], d + 2);
+        };
+        if (act) {
+            fetch(xb, dBo + o, rb);
+            fetch(xc, dCo + o, rc);
+        }
+        for (int g = 0; g < s.G; ++g, o += s.N) {
+            const bool more = act && g + 1 < s.G;
             float2 x[4], d[4];
-            widen4(raw[0], x);
-            widen4(raw[1], x + 2);
-            widen4(raw[2], d);
-            widen4(raw[3], d + 2);
+            row(rb, x, d);
+            xb += s.N;
+            if (more) fetch(xb, dBo + o + s.N, rb);
             row_backward<LANES>(s, l, inv_n, turn, x, d, wb, gb);
             if (act) store_lane<WIDE>(dB + o, l, d);
-            widen4(raw[4], x);
-            widen4(raw[5], x + 2);
-            widen4(raw[6], d);
-            widen4(raw[7], d + 2);
+            row(rc, x, d);
+            xc += s.N;
+            if (more) fetch(xc, dCo + o + s.N, rc);
             row_backward<LANES>(s, l, inv_n, turn, x, d, wc, gc);
             if (act) store_lane<WIDE>(dC + o, l, d);
         }
