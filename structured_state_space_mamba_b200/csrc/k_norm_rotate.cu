@@ -34,6 +34,7 @@ constexpr int kWarps = kThreads / 32;
 // inner loop, and it is the faster for the loads that they have in flight)
 template <typename T> constexpr int kForwardPerSm = sizeof(T) == 2 ? 7 : 5;
 constexpr int kBackwardPerSm = 4;
+constexpr int kAnyPerSm = 8;
 
 // four values as they lie in memory, and as numbers
 template <typename T> struct Raw;
@@ -389,36 +390,28 @@ norm_rotate_backward_kernel(const __grid_constant__ RotateShape s, const T *__re
 }
 
 // ---------------------------------------------------------------------------
-// any dstate, rotary and alignment: one warp a row of B or C, single values.
-// Pair j is on lane j % 32 (at most four a lane), and so are the values behind
-// the rotary ones.
+// any dstate, rotary and alignment: one warp a token, row after row of B and C,
+// single values.  Pair j is on lane j % 32 (at most four a lane), and so are the
+// values behind the rotary ones; the angles are formed once a token.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-struct Row {
-    int64_t tok;
-    int g;
-    bool isC;
-};
-__device__ __forceinline__ Row row_of(const RotateShape &s, int64_t r) {
-    Row w;
-    w.isC = r & 1;
-    r >>= 1;
-    w.tok = r / s.G;
-    w.g = int(r - w.tok * s.G);
-    return w;
-}
 __device__ __forceinline__ void pair_of(const RotateShape &s, int j, int &p, int &q) {
     p = s.interleaved ? 2 * j : j;
     q = s.interleaved ? 2 * j + 1 : j + s.rotary / 2;
 }
 template <typename T>
-__device__ __forceinline__ const T *row_ptr(const RotateShape &s, const T *Bm, const T *Cm, const Row &w) {
-    const int64_t b = w.tok / s.T, t = w.tok - b * s.T;
-    return (w.isC ? Cm + b * s.C_batch + t * s.C_token : Bm + b * s.B_batch + t * s.B_token) + int64_t(w.g) * s.N;
+__device__ __forceinline__ void any_angles(const RotateShape &s, const float *inv_freq, double pos, int lane,
+                                           float (&sn)[4], float (&cs)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (32 * k >= s.rotary / 2) break;
+        const int j = lane + 32 * k;
+        if (j < s.rotary / 2) sincos_turn<T>(turn_fraction(pos, __ldg(inv_freq + j)), sn[k], cs[k]);
+    }
 }
 
 template <typename T>
@@ -428,37 +421,44 @@ norm_rotate_any_kernel(const __grid_constant__ RotateShape s, const T *__restric
                        const float *__restrict__ wB, const float *__restrict__ wC, T *__restrict__ Bo,
                        T *__restrict__ Co) {
     const int lane = threadIdx.x & 31;
-    const int64_t rows = s.tokens * s.G * 2;
-    for (int64_t r = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); r < rows; r += int64_t(gridDim.x) * kWarps) {
-        const Row w = row_of(s, r);
-        const T *x = row_ptr(s, Bm, Cm, w);
-        T *o = (w.isC ? Co : Bo) + (w.tok * s.G + w.g) * s.N;
-        const float *wt = w.isC ? wC : wB;
-        float ss = 0.f;
-        for (int n = lane; n < s.N; n += 32) {
-            const float v = to_f32<T>(x[n]);
-            ss = fmaf(v, v, ss);
+    const float inv_n = 1.f / float(s.N);
+    for (int64_t tok = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); tok < s.tokens;
+         tok += int64_t(gridDim.x) * kWarps) {
+        int64_t ob, oc;
+        token_place(s, tok, ob, oc);
+        float sn[4], cs[4];
+        any_angles<T>(s, inv_freq, double(__ldg(positions + tok)), lane, sn, cs);
+        for (int row = blockIdx.y; row < 2 * s.G; row += gridDim.y) {  // B's and C's in turn
+            const bool isC = row & 1;
+            const int64_t at = int64_t(row >> 1) * s.N;
+            const T *x = isC ? Cm + oc + at : Bm + ob + at;
+            T *o = (isC ? Co : Bo) + tok * s.G * s.N + at;
+            const float *wt = isC ? wC : wB;
+            float ss = 0.f;
+            for (int n = lane; n < s.N; n += 32) {
+                const float v = to_f32<T>(x[n]);
+                ss = fmaf(v, v, ss);
+            }
+            const float rstd = rsqrtf(fmaf(warp_sum(ss), inv_n, s.eps));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (32 * k >= s.rotary / 2) break;
+                const int j = lane + 32 * k;
+                if (j >= s.rotary / 2) continue;
+                int p, q;
+                pair_of(s, j, p, q);
+                const float a = to_f32<T>(x[p]) * rstd * (wt ? __ldg(wt + p) : 1.f);
+                const float b = to_f32<T>(x[q]) * rstd * (wt ? __ldg(wt + q) : 1.f);
+                o[p] = from_f32<T>(a * cs[k] - b * sn[k]);
+                o[q] = from_f32<T>(a * sn[k] + b * cs[k]);
+            }
+            for (int n = s.rotary + lane; n < s.N; n += 32)
+                o[n] = from_f32<T>(to_f32<T>(x[n]) * rstd * (wt ? __ldg(wt + n) : 1.f));
         }
-        const float rstd = rsqrtf(warp_sum(ss) / float(s.N) + s.eps);
-        const double pos = double(__ldg(positions + w.tok));
-        for (int j = lane; j < s.rotary / 2; j += 32) {
-            int p, q;
-            pair_of(s, j, p, q);
-            float sn, cs;
-            sincos_turn<T>(turn_fraction(pos, __ldg(inv_freq + j)), sn, cs);
-            const float a = to_f32<T>(x[p]) * rstd * (wt ? __ldg(wt + p) : 1.f);
-            const float b = to_f32<T>(x[q]) * rstd * (wt ? __ldg(wt + q) : 1.f);
-            o[p] = from_f32<T>(a * cs - b * sn);
-            o[q] = from_f32<T>(a * sn + b * cs);
-        }
-        for (int n = s.rotary + lane; n < s.N; n += 32)
-            o[n] = from_f32<T>(to_f32<T>(x[n]) * rstd * (wt ? __ldg(wt + n) : 1.f));
     }
 }
 
-// A warp's rows all lie on one of B and C (rows step by an even number), so its
-// sums for that tensor's weight stay in registers: four pairs and eight values
-// behind them a lane.
+// The weights' gradients gather in shared memory, a value always by the same lane.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 norm_rotate_backward_any_kernel(const __grid_constant__ RotateShape s, const T *__restrict__ dBo,
@@ -466,69 +466,74 @@ norm_rotate_backward_any_kernel(const __grid_constant__ RotateShape s, const T *
                                 const int64_t *__restrict__ positions, const float *__restrict__ inv_freq,
                                 const float *__restrict__ wB, const float *__restrict__ wC, T *__restrict__ dB,
                                 T *__restrict__ dC, float *__restrict__ part) {
-    __shared__ float red[kWarps][256];
+    __shared__ float red[kWarps][2][256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int n = lane; n < 256; n += 32) red[warp][n] = 0.f;
+    const float inv_n = 1.f / float(s.N);
+    for (int n = lane; n < 256; n += 32) red[warp][0][n] = red[warp][1][n] = 0.f;
     __syncwarp();
-    const int64_t rows = s.tokens * s.G * 2;
-    for (int64_t r = int64_t(blockIdx.x) * kWarps + warp; r < rows; r += int64_t(gridDim.x) * kWarps) {
-        const Row w = row_of(s, r);
-        const T *x = row_ptr(s, Bm, Cm, w);
-        const int64_t off = (w.tok * s.G + w.g) * s.N;
-        const T *d = (w.isC ? dCo : dBo) + off;
-        T *o = (w.isC ? dC : dB) + off;
-        const float *wt = w.isC ? wC : wB;
-        const double pos = double(__ldg(positions + w.tok));
-        float ss = 0.f, dot = 0.f;
-        float z0[4], z1[4];  // the cotangent, rotated back
+    for (int64_t tok = int64_t(blockIdx.x) * kWarps + warp; tok < s.tokens; tok += int64_t(gridDim.x) * kWarps) {
+        int64_t ob, oc;
+        token_place(s, tok, ob, oc);
+        float sn[4], cs[4];
+        any_angles<T>(s, inv_freq, double(__ldg(positions + tok)), lane, sn, cs);
+        for (int row = 0; row < 2 * s.G; ++row) {
+            const bool isC = row & 1;
+            const int64_t at = int64_t(row >> 1) * s.N, off = tok * s.G * s.N + at;
+            const T *x = isC ? Cm + oc + at : Bm + ob + at, *d = (isC ? dCo : dBo) + off;
+            T *o = (isC ? dC : dB) + off;
+            const float *wt = isC ? wC : wB;
+            float *acc = red[warp][isC];
+            float ss = 0.f, dot = 0.f;
+            float z0[4], z1[4], x0[4], x1[4];  // the cotangent, rotated back, and the values
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int j = lane + 32 * k;
-            z0[k] = z1[k] = 0.f;
-            if (j >= s.rotary / 2) continue;
-            int p, q;
-            pair_of(s, j, p, q);
-            float sn, cs;
-            sincos_turn<T>(turn_fraction(pos, __ldg(inv_freq + j)), sn, cs);
-            const float d0 = to_f32<T>(d[p]), d1 = to_f32<T>(d[q]), x0 = to_f32<T>(x[p]), x1 = to_f32<T>(x[q]);
-            z0[k] = d0 * cs + d1 * sn;
-            z1[k] = d1 * cs - d0 * sn;
-            ss = fmaf(x0, x0, fmaf(x1, x1, ss));
-            dot = fmaf(z0[k] * (wt ? __ldg(wt + p) : 1.f), x0, dot);
-            dot = fmaf(z1[k] * (wt ? __ldg(wt + q) : 1.f), x1, dot);
-        }
-        for (int n = s.rotary + lane; n < s.N; n += 32) {
-            const float v = to_f32<T>(x[n]);
-            ss = fmaf(v, v, ss);
-            dot = fmaf(to_f32<T>(d[n]) * (wt ? __ldg(wt + n) : 1.f), v, dot);
-        }
-        const float rstd = rsqrtf(warp_sum(ss) / float(s.N) + s.eps);
-        const float m = warp_sum(dot) / float(s.N) * rstd * rstd;
+            for (int k = 0; k < 4; ++k) {
+                if (32 * k >= s.rotary / 2) break;
+                const int j = lane + 32 * k;
+                z0[k] = z1[k] = x0[k] = x1[k] = 0.f;
+                if (j >= s.rotary / 2) continue;
+                int p, q;
+                pair_of(s, j, p, q);
+                const float d0 = to_f32<T>(d[p]), d1 = to_f32<T>(d[q]);
+                x0[k] = to_f32<T>(x[p]);
+                x1[k] = to_f32<T>(x[q]);
+                z0[k] = d0 * cs[k] + d1 * sn[k];
+                z1[k] = d1 * cs[k] - d0 * sn[k];
+                ss = fmaf(x0[k], x0[k], fmaf(x1[k], x1[k], ss));
+                dot = fmaf(z0[k] * (wt ? __ldg(wt + p) : 1.f), x0[k], dot);
+                dot = fmaf(z1[k] * (wt ? __ldg(wt + q) : 1.f), x1[k], dot);
+            }
+            for (int n = s.rotary + lane; n < s.N; n += 32) {
+                const float v = to_f32<T>(x[n]);
+                ss = fmaf(v, v, ss);
+                dot = fmaf(to_f32<T>(d[n]) * (wt ? __ldg(wt + n) : 1.f), v, dot);
+            }
+            const float rstd = rsqrtf(fmaf(warp_sum(ss), inv_n, s.eps));
+            const float m = warp_sum(dot) * inv_n * rstd * rstd;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int j = lane + 32 * k;
-            if (j >= s.rotary / 2) continue;
-            int p, q;
-            pair_of(s, j, p, q);
-            const float x0 = to_f32<T>(x[p]), x1 = to_f32<T>(x[q]);
-            red[warp][p] = fmaf(z0[k], x0 * rstd, red[warp][p]);
-            red[warp][q] = fmaf(z1[k], x1 * rstd, red[warp][q]);
-            o[p] = from_f32<T>(rstd * (z0[k] * (wt ? __ldg(wt + p) : 1.f) - x0 * m));
-            o[q] = from_f32<T>(rstd * (z1[k] * (wt ? __ldg(wt + q) : 1.f) - x1 * m));
-        }
-        for (int n = s.rotary + lane; n < s.N; n += 32) {
-            const float v = to_f32<T>(x[n]), z = to_f32<T>(d[n]);
-            red[warp][n] = fmaf(z, v * rstd, red[warp][n]);
-            o[n] = from_f32<T>(rstd * (z * (wt ? __ldg(wt + n) : 1.f) - v * m));
+            for (int k = 0; k < 4; ++k) {
+                if (32 * k >= s.rotary / 2) break;
+                const int j = lane + 32 * k;
+                if (j >= s.rotary / 2) continue;
+                int p, q;
+                pair_of(s, j, p, q);
+                acc[p] = fmaf(z0[k], x0[k] * rstd, acc[p]);
+                acc[q] = fmaf(z1[k], x1[k] * rstd, acc[q]);
+                o[p] = from_f32<T>(rstd * (z0[k] * (wt ? __ldg(wt + p) : 1.f) - x0[k] * m));
+                o[q] = from_f32<T>(rstd * (z1[k] * (wt ? __ldg(wt + q) : 1.f) - x1[k] * m));
+            }
+            for (int n = s.rotary + lane; n < s.N; n += 32) {
+                const float v = to_f32<T>(x[n]), z = to_f32<T>(d[n]);
+                acc[n] = fmaf(z, v * rstd, acc[n]);
+                o[n] = from_f32<T>(rstd * (z * (wt ? __ldg(wt + n) : 1.f) - v * m));
+            }
         }
     }
     if (!part) return;
     __syncthreads();
-    // even warps hold B's sums, odd ones C's
     for (int o = threadIdx.x; o < 2 * s.N; o += kThreads) {
         const int which = o >= s.N, j = which ? o - s.N : o;
         float sum = 0.f;
-        for (int v = which; v < kWarps; v += 2) sum += red[v][j];
+        for (int v = 0; v < kWarps; ++v) sum += red[v][which][j];
         part[int64_t(blockIdx.x) * 2 * s.N + o] = sum;
     }
 }
@@ -607,8 +612,10 @@ cudaError_t forward_typed(const RotateShape &s, const T *Bm, const T *Cm, const 
                 <<<grid, kThreads, 0, st>>>(s, Bm, Cm, positions, inv_freq, wB, wC, Bo, Co);
         });
     } else {
-        const int64_t need = (s.tokens * s.G * 2 + kWarps - 1) / kWarps;
-        norm_rotate_any_kernel<T><<<unsigned(even_blocks(need, 16)), kThreads, 0, st>>>(
+        const unsigned gx = unsigned(even_blocks((s.tokens + kWarps - 1) / kWarps, kAnyPerSm));
+        int64_t gy = int64_t(device_sm_count()) * kAnyPerSm / gx;
+        if (gy > 2 * s.G) gy = 2 * s.G;
+        norm_rotate_any_kernel<T><<<dim3(gx, unsigned(gy < 1 ? 1 : gy)), kThreads, 0, st>>>(
             s, Bm, Cm, positions, inv_freq, wB, wC, Bo, Co);
     }
     return cudaGetLastError();
