@@ -9,7 +9,8 @@ the library is missing.
 from __future__ import annotations
 
 __all__ = ["forward", "forward_ws", "workspace_bytes", "workspace_layout", "lib_path",
-           "SSDError"]
+           "SSDError", "Packed8", "pack8", "unpack8", "glr_forward", "glr_backward", "glr_step", "norm_rotate",
+           "norm_rotate_backward", "backward_packed8"]
 
 
 def __getattr__(name):

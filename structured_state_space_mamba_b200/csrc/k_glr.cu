@@ -23,15 +23,14 @@
 //
 // What bounds it.  Compulsory traffic is 8 bytes a value forwards in bf16 and 14
 // backwards (11 from checkpoints).  On 4 x 4096 x 5120 the forward pass takes
-// 140 us on the device, 4.8 TB/s: a pair of channels costs 79 instructions, of
+// 140 us on the device, 4.8 TB/s: a pair of channels costs 72 instructions, of
 // which the packed ones (two cycles each) and the scalar ones fill the fp32 pipe
-// for about 68 cycles and eight special functions theirs for 65, of the 120
-// cycles that pass; issue slots are 60 % busy, and neither more warps (four groups
-// of 56 registers: 144 us; 16 warps of four tokens: 162 us) nor an earlier hand-out
-// of the states changed that.  Backwards it is 164 instructions and 16 special
-// functions a pair, about twice the time.  With few chains (1 x 65536 x 2048: 32 of
-// them for 444 groups) tiles of one chain wait for each other's sums through L2,
-// three to four trips a tile: 331 us.
+// for about 65 cycles and eight special functions theirs for as many, of the 115
+// cycles that pass.  More warps did not change that (four groups of 56 registers:
+// 144 us; 16 warps of four tokens: 162 us), nor an earlier hand-out of the states.
+// Backwards it is 150 instructions and 16 special functions a pair, about twice the
+// time.  With few chains (1 x 65536 x 2048: 32 of them for 444 groups) the tiles of
+// a chain wait for each other's sums through L2, three to four trips a tile: 330 us.
 #include "common.cuh"
 #include "glr.h"
 #include "pack8.cuh"
