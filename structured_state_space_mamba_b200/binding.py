@@ -671,10 +671,10 @@ def _glr_forward(st, dims, x, r, i, A, init_state, cu, rows, return_final_state,
     lib, C = load(), dims.channels
     cu_p, nseq = (None, 0) if cu is None else (cu.ctypes.data, rows)
     y = torch.empty_like(x) if out is None else out
-    final = A.new_empty((rows, C)) if return_final_state else None
+    final = A.new_empty(rows, C) if return_final_state else None
     states = packed = pk = None
     if save is not None:
-        states = A.new_empty((lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C))
+        states = A.new_empty(lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C)
         if save == "packed8":
             packed = [Packed8.empty_like(x) for _ in range(3)]
             pk = (_Packed8 * 3)(*(p._c() for p in packed))
@@ -720,7 +720,7 @@ def _glr_backward(st, dims, dy, saved, packed, dfinal_state, return_dinit_state,
           (lib.ssd_glr_chunk_rows(ctypes.byref(dims), cu_p, nseq), C))
     dx, dr, di = torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(dy)
     dA = torch.empty_like(saved.A)
-    dinit = saved.A.new_empty((saved.rows, C)) if return_dinit_state else None
+    dinit = saved.A.new_empty(saved.rows, C) if return_dinit_state else None
     if packed:
         x = r = i = None
         pk = (_Packed8 * 3)(saved.x._c(), saved.r._c(), saved.i._c())

@@ -375,25 +375,24 @@ constexpr int kWindow = 4;  // predecessors that a tile looks back over
 
 // The state that enters the tile, for one warp (t.rank > 0): the outgoing state of
 // the nearest predecessor that has published it, taken through the sums of those
-// in between, in their order.  Every round fetches all of them, so that a round
-// is one trip through L2, and every lane goes by its own words.  Gives up with
-// the error word set after kWaitLimitNs.
+// in between, in their order.  Every round fetches what is still missing, so that
+// a round is one trip through L2, and every lane goes by its own words.  Gives
+// up with the error word set after kWaitLimitNs.
 __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, int lane, float2 &h,
                                           unsigned int *err) {
     const int window = min(t.rank, kWindow);
     uint64_t t0 = 0;
+    float4 sums[kWindow - 1];
+#pragma unroll
+    for (int d = 0; d < kWindow - 1; ++d) sums[d] = make_float4(0.f, 0.f, 0.f, __uint_as_float(kUnset));
     for (uint32_t n = 0;; ++n) {
         float2 state[kWindow];
-        float4 sums[kWindow - 1];
 #pragma unroll
         for (int d = 0; d < kWindow; ++d) {
             const int64_t tile = t.tile - int64_t(d + 1) * t.stride;
             state[d] = both(__uint_as_float(kUnset));
             if (d < window) state[d] = get_state(ws, tile, lane);
-            if (d < kWindow - 1) {
-                sums[d] = make_float4(0.f, 0.f, 0.f, __uint_as_float(kUnset));
-                if (d < window) sums[d] = get_sums(ws, tile, lane);
-            }
+            if (d < kWindow - 1 && d < window && !set(sums[d])) sums[d] = get_sums(ws, tile, lane);
         }
         bool ok = false;
 #pragma unroll
