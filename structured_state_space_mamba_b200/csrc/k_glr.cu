@@ -530,7 +530,10 @@ struct Tickets {
 constexpr int kGroups = 3;
 constexpr int kBlock = kGroups * kGroupThreads;
 
-// The tiles of a group, in a ring: tile k + NS + 2 is set while k is finished.
+// The tiles of a group, in a ring: tile k + NS + 1 is set before the starts of tile k
+// are handed out, with which it becomes visible, and is copied from after the gates
+// of tile k + 1.  No ticket is taken earlier than that: a group that lags holds up
+// the chains of all the tiles that it has taken.
 constexpr int kInfos = 8;
 struct Sync {
     uint64_t parts, ready;
@@ -568,7 +571,7 @@ struct FwdPlan {
         // products and sums of the warps' tokens; in their place then the states before them
         float4 part[kWarps][32];
         Sync sync;
-        static_assert(kStages + 3 <= kInfos, "a tile's place is taken while it is in use");
+        static_assert(kStages + 2 <= kInfos, "a tile's place is taken while it is in use");
     };
     static constexpr int smem = kGroups * sizeof(Smem);
     static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
@@ -596,18 +599,18 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         tc::mbar_init(&sync.parts, kWarps);
         tc::mbar_init(&sync.ready, 1);
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
     if (warp == kWarps) {  // the scan warp
-        uint32_t next = 0;  // a ticket taken one tile ago
+        uint32_t next = 0;  // a ticket taken a tile ago
         if (lane == 0) next = tickets.take();
         for (int k = 0;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
-            uint32_t later = 0;
-            if (lane == 0) later = tickets.take();
+            if (lane == 0) set_tile(k + NS + 1, next);
+            __syncwarp();
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = both(0.f);
@@ -637,10 +640,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             arrive_warp(&sync.ready, lane);
             if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, start, a0, a1);
             if (t.last && p.fin) store2<float, VEC>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
-            if (lane == 0) {
-                set_tile(k + NS + 2, next);
-                next = later;
-            }
+            if (lane == 0) next = tickets.take();
             __syncwarp();
         }
         return;
@@ -773,7 +773,7 @@ struct BwdPlan {
         float2 rpart[kWarps][32];  // reverse sums
         float2 dA[2][kWarps][32];
         Sync sync;
-        static_assert(kStages + 3 <= kInfos, "a tile's place is taken while it is in use");
+        static_assert(kStages + 2 <= kInfos, "a tile's place is taken while it is in use");
     };
     static constexpr int smem = kGroups * sizeof(Smem);
     static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
@@ -803,7 +803,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         tc::mbar_init(&sync.parts, kWarps);
         tc::mbar_init(&sync.ready, 1);
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 2; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
@@ -817,14 +817,14 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[k & 1][w][lane]);
             store2<float, VEC>(p.dA_part + t.chunk * C + c, sum, c < C, c + 1 < C);
         };
-        uint32_t next = 0;  // a ticket taken one tile ago
+        uint32_t next = 0;  // a ticket taken a tile ago
         if (lane == 0) next = tickets.take();
         int k = 0;
         for (;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
-            uint32_t later = 0;
-            if (lane == 0) later = tickets.take();
+            if (lane == 0) set_tile(k + NS + 1, next);
+            __syncwarp();
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = load2<VEC>(p.states + t.chunk * C + c, a0, a1), K = both(0.f);
@@ -861,10 +861,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
             if (k >= 1) sum_dA(k - 1);
             __syncwarp();
-            if (lane == 0) {
-                set_tile(k + NS + 2, next);
-                next = later;
-            }
+            if (lane == 0) next = tickets.take();
             __syncwarp();
         }
         if (k > 0) {  // the last tile: its warps say when they are through
