@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "glr.h"
 #include "kernels.h"
+#include "tma_host.h"
 
 // Device word set by tensor-core kernels whose bounded waits expired.
 __device__ unsigned int g_ssd_device_error;
@@ -39,6 +40,7 @@ unsigned int *device_error_word() {
         return nullptr;
     }
     std::call_once(g_err_once[dev], [dev] {
+        const SetupWhileCapturing relaxed;
         void *p = nullptr;
         if (cudaGetSymbolAddress(&p, g_ssd_device_error) == cudaSuccess)
             g_err_ptr[dev] = static_cast<unsigned int *>(p);
@@ -66,6 +68,7 @@ std::once_flag g_pool_once[kMaxDevices];
 
 cudaMemPool_t workspace_pool(int dev) {
     std::call_once(g_pool_once[dev], [dev] {
+        const ssd::SetupWhileCapturing relaxed;
         cudaMemPoolProps props;
         std::memset(&props, 0, sizeof(props));
         props.allocType = cudaMemAllocationTypePinned;

@@ -63,6 +63,7 @@ bool smem_attr_once(const void *kernel, int bytes) {
     const auto key = std::make_pair(dev, kernel);
     auto it = done.find(key);
     if (it != done.end() && it->second >= bytes) return true;
+    const SetupWhileCapturing relaxed;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess) {
         cudaGetLastError();

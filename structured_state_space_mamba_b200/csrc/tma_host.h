@@ -28,4 +28,19 @@ bool smem_attr_once(const void *kernel, int bytes);
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 
+// One-time set-up (a symbol's address, a pool, a kernel's shared-memory limit) may
+// load code or map memory, which a capture in the default mode forbids to every
+// thread's calls and which would end the capture of a process's first call.  None
+// of it is work on a stream: for its duration this thread's mode is relaxed.
+class SetupWhileCapturing {
+  public:
+    SetupWhileCapturing() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~SetupWhileCapturing() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    SetupWhileCapturing(const SetupWhileCapturing &) = delete;
+    SetupWhileCapturing &operator=(const SetupWhileCapturing &) = delete;
+
+  private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
 }  // namespace ssd
