@@ -378,8 +378,9 @@ constexpr int kWindow = 4;  // predecessors that a tile looks back over
 // in between, in their order.  Every round fetches what is still missing, so that
 // a round is one trip through L2, and every lane goes by its own words.  Gives
 // up with the error word set after kWaitLimitNs.
+template <typename F>
 __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, int lane, float2 &h,
-                                          unsigned int *err) {
+                                          unsigned int *err, F &&meanwhile) {
     const int window = min(t.rank, kWindow);
     uint64_t t0 = 0;
     float4 sums[kWindow - 1];
@@ -406,6 +407,7 @@ __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, i
             }
         }
         if (__all_sync(0xffffffffu, ok)) return true;
+        meanwhile();
         if ((n & 15u) == 15u) {
             const uint64_t now = tc::global_ns();
             if (t0 == 0) t0 = now;
@@ -530,15 +532,34 @@ struct Tickets {
 constexpr int kGroups = 3;
 constexpr int kBlock = kGroups * kGroupThreads;
 
-// The tiles of a group, in a ring: tile k + NS + 1 is set before the starts of tile k
-// are handed out, with which it becomes visible, and is copied from after the gates
-// of tile k + 1.  No ticket is taken earlier than that: a group that lags holds up
-// the chains of all the tiles that it has taken.
+// The tiles of a group, in a ring: a tile is set before the starts of the last tile
+// but one before its copies begin are handed out, with which it becomes visible (tile
+// k + NS + 1 before those of tile k with NS stages).  No ticket is taken earlier than
+// that: a group that lags holds up the chains of all the tiles that it has taken.
 constexpr int kInfos = 8;
+template <int SLOTS>
 struct Sync {
-    uint64_t parts, ready;
+    uint64_t parts[SLOTS], ready[SLOTS];
     Tile tile[kInfos];
 };
+// whether a phase is over, for a whole warp and without waiting
+__device__ __forceinline__ bool passed(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred q; mbarrier.test_wait.parity.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
+                 : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
+    return __all_sync(0xffffffffu, ok != 0);
+}
+// the warps' products and sums, joined
+__device__ __forceinline__ void join(const float4 (&part)[kWarps][32], int lane, float2 &P, float2 &S) {
+    P = both(1.f);
+    S = both(0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float4 q = part[w][lane];
+        P = mul(P, make_float2(q.x, q.y));
+        S = fma(make_float2(q.x, q.y), S, make_float2(q.z, q.w));
+    }
+}
 __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive_cnt(bar, 1);
@@ -562,16 +583,25 @@ struct FwdArgs {
 };
 template <typename T>
 struct FwdPlan {
-    static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+    // A tile ahead: the gates of tile k + 1 are formed, and its sums published, while
+    // tile k waits for its state; the terms of tile k stay in shared memory meanwhile.
+    // Few chains need it: there a tile waits for the sums of several groups, and those
+    // used to wait for their own states first.  1 x 65536 x 2048 in bf16: 336 -> 270 us;
+    // 4 x 4096 x 5120: 140 -> 137.  In place of the second stage of copies; inputs in
+    // fp32 leave no room for the terms.
+    static constexpr bool kHold = sizeof(T) == 2;
+    static constexpr int kSlots = kHold ? 2 : 1;
+    static constexpr int kLead = kHold ? 3 : 2;  // tiles that are set before the first
     struct Stage {
         T x[kWarpVals], r[kWarpVals], i[kWarpVals];
     };
     struct alignas(128) Smem {
-        Stage stage[kStages][kWarps];
+        Stage stage[kWarps];
         // products and sums of the warps' tokens; in their place then the states before them
-        float4 part[kWarps][32];
-        Sync sync;
-        static_assert(kStages + 2 <= kInfos, "a tile's place is taken while it is in use");
+        float4 part[kSlots][kWarps][32];
+        float4 held[kHold ? kWarps : 1][kHold ? kTok : 1][32];
+        Sync<kSlots> sync;
+        static_assert(kLead + 2 <= kInfos, "a tile's place is taken while it is in use");
     };
     static constexpr int smem = kGroups * sizeof(Smem);
     static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
@@ -581,12 +611,12 @@ template <typename T, bool VEC, bool PACK>
 __global__ void __launch_bounds__(kBlock, 1)
 glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     using Plan = FwdPlan<T>;
-    constexpr int NS = Plan::kStages;
+    constexpr int SL = Plan::kSlots, LEAD = Plan::kLead;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
     const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
     typename Plan::Smem &sm = reinterpret_cast<typename Plan::Smem *>(smem_raw)[group];
-    Sync &sync = sm.sync;
+    auto &sync = sm.sync;
     const int C = p.s.C;
     Tickets tickets(p.ws.ticket, p.tiles, kGroups, group);
     auto set_tile = [&](int k, uint32_t raw) {
@@ -596,48 +626,60 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         else t.tile = -1;
     };
     if (warp == kWarps && lane == 0) {
-        tc::mbar_init(&sync.parts, kWarps);
-        tc::mbar_init(&sync.ready, 1);
+        for (int n = 0; n < SL; ++n) {
+            tc::mbar_init(&sync.parts[n], kWarps);
+            tc::mbar_init(&sync.ready[n], 1);
+        }
         tc::fence_mbar_init();
-        for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
+        for (int k = 0; k < LEAD; ++k) set_tile(k, tickets.take());
     }
     __syncthreads();
 
     if (warp == kWarps) {  // the scan warp
         uint32_t next = 0;  // a ticket taken a tile ago
+        bool published = false;  // this tile's sums, during the wait of the one before
         if (lane == 0) next = tickets.take();
         for (int k = 0;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
-            if (lane == 0) set_tile(k + NS + 1, next);
+            if (lane == 0) set_tile(k + LEAD, next);
             __syncwarp();
             const int c = t.ct * kGlrCols + 2 * lane;
             const bool a0 = c < C, a1 = c + 1 < C;
             float2 h = both(0.f);
             if (!t.first) h = get_state(p.ws, t.tile - int64_t(t.stride), lane);  // it may be there by now
             else if (p.h0) h = load2<VEC>(p.h0 + int64_t(t.row) * C + c, a0, a1);
-            tc::mbar_wait(&sync.parts, k & 1, p.err);
-            float2 P = both(1.f), S = both(0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 q = sm.part[w][lane];
-                P = mul(P, make_float2(q.x, q.y));
-                S = fma(make_float2(q.x, q.y), S, make_float2(q.z, q.w));
-            }
+            auto &part = sm.part[k % SL];
+            tc::mbar_wait(&sync.parts[k % SL], (k / SL) & 1, p.err);
+            float2 P, S;
+            join(part, lane, P, S);
             if (!t.first && !__all_sync(0xffffffffu, set(h))) {
-                if (!t.last) put_sums(p.ws, t.tile, lane, P, S);
-                look_back(p.ws, t, lane, h, p.err);
+                if (!t.last && !published) put_sums(p.ws, t.tile, lane, P, S);
+                published = false;
+                look_back(p.ws, t, lane, h, p.err, [&] {
+                    if (SL == 1 || published) return;
+                    const Tile &n = sync.tile[(k + 1) & (kInfos - 1)];
+                    if (n.tile < 0 || n.first || n.last ||
+                        !passed(&sync.parts[(k + 1) % SL], ((k + 1) / SL) & 1))
+                        return;
+                    float2 P1, S1;
+                    join(sm.part[(k + 1) % SL], lane, P1, S1);
+                    put_sums(p.ws, n.tile, lane, P1, S1);
+                    published = true;
+                });
+            } else {
+                published = false;
             }
             const float2 out = fma(P, h, S);
             if (!t.last) put_state(p.ws, t.tile, lane, out);
             const float2 start = h;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float4 q = sm.part[w][lane];
-                *reinterpret_cast<float2 *>(&sm.part[w][lane]) = h;
+                const float4 q = part[w][lane];
+                *reinterpret_cast<float2 *>(&part[w][lane]) = h;
                 h = fma(make_float2(q.x, q.y), h, make_float2(q.z, q.w));
             }
-            arrive_warp(&sync.ready, lane);
+            arrive_warp(&sync.ready[k % SL], lane);
             if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, start, a0, a1);
             if (t.last && p.fin) store2<float, VEC>(p.fin + int64_t(t.row) * C + c, out, a0, a1);
             if (lane == 0) next = tickets.take();
@@ -649,7 +691,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     auto load = [&](int k) {
         const Tile &t = sync.tile[k & (kInfos - 1)];
         if (t.tile >= 0) {
-            typename Plan::Stage &st = sm.stage[k % NS][warp];
+            typename Plan::Stage &st = sm.stage[warp];
             T *const dst[3] = {st.x, st.r, st.i};
             const T *const src[3] = {p.x, p.r, p.i};
             fill<T, VEC, 3>(dst, src, t, C, warp, lane);
@@ -662,16 +704,13 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
     const Held hd;
-    for (int k = 0; k < NS; ++k) load(k);
-    float2 A = rates(0);
-    for (int k = 0;; ++k) {
-        const Tile &t = sync.tile[k & (kInfos - 1)];
-        if (t.tile < 0) break;
+    // the gates of a tile, and their product and sum
+    auto gates = [&](const Tile &t, float2 A, float2 (&e1)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32]) {
         const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
-        copy_wait<NS - 1>();
+        copy_wait<0>();
         __syncwarp();
-        const typename Plan::Stage &st = sm.stage[k % NS][warp];
+        const typename Plan::Stage &st = sm.stage[warp];
         if (PACK) {
             const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
             if constexpr (VEC) {
@@ -699,7 +738,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
                 }
             }
         }
-        float2 e1[kTok], u[kTok], P = both(1.f), S = both(0.f);
+        float2 P = both(1.f), S = both(0.f);
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
             const int o = j * kGlrCols + 2 * lane;
@@ -715,27 +754,56 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             P = fma(e1[j], P, P);
             S = advance(S, e1[j], u[j]);
         }
-        sm.part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
-        arrive_warp(&sync.parts, lane);  // and this warp's part of the stage is read
-        load(k + NS);
-        A = rates(k + 1);
+        part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+    };
+    // a tile's tokens from the state before them; term(j): e^l - 1 and the input's part
+    auto finish = [&](const Tile &t, const float4 (&part)[kWarps][32], auto term) {
         T *y = p.y + (t.base + (int64_t(warp * kTok) * C + 2 * lane));
         const bool even = C % 2 == 0;
-        tc::mbar_wait(&sync.ready, k & 1, p.err);
-        float2 h = *reinterpret_cast<const float2 *>(&sm.part[warp][lane]);
-        if (t.full) {
+        const int c = t.ct * kGlrCols + 2 * lane, ntok = t.ntok - warp * kTok;
+        const bool full = t.full;
+        float2 h = *reinterpret_cast<const float2 *>(&part[warp][lane]);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j, y += C) {
-                h = advance(h, e1[j], u[j]);
-                store2<T, VEC>(y, h, true, true, even);
+        for (int j = 0; j < kTok; ++j, y += C) {
+            const float4 q = term(j);
+            h = advance(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
+            if (full) store2<T, VEC>(y, h, true, true, even);
+            else if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C, even);
+        }
+    };
+    load(0);
+    float2 A = rates(0);
+    if constexpr (!Plan::kHold) {
+        for (int k = 0;; ++k) {
+            const Tile &t = sync.tile[k & (kInfos - 1)];
+            if (t.tile < 0) break;
+            float2 e1[kTok], u[kTok];
+            gates(t, A, e1, u, sm.part[0]);
+            arrive_warp(&sync.parts[0], lane);  // and this warp's part of the stage is read
+            load(k + 1);
+            A = rates(k + 1);
+            tc::mbar_wait(&sync.ready[0], k & 1, p.err);
+            finish(t, sm.part[0], [&](int j) { return make_float4(e1[j].x, e1[j].y, u[j].x, u[j].y); });
+        }
+    } else {
+        for (int k = -1;; ++k) {
+            const Tile &t = sync.tile[k & (kInfos - 1)], &n = sync.tile[(k + 1) & (kInfos - 1)];
+            if (k >= 0 && t.tile < 0) break;
+            const bool more = n.tile >= 0;
+            float2 e1[kTok], u[kTok];
+            if (more) {
+                gates(n, A, e1, u, sm.part[(k + 1) % SL]);
+                arrive_warp(&sync.parts[(k + 1) % SL], lane);
+                load(k + 2);
+                A = rates(k + 2);
             }
-        } else {
-            const int c = t.ct * kGlrCols + 2 * lane;
+            if (k >= 0) {
+                tc::mbar_wait(&sync.ready[k % SL], (k / SL) & 1, p.err);
+                finish(t, sm.part[k % SL], [&](int j) { return sm.held[warp][j][lane]; });
+            }
+            if (!more) break;
 #pragma unroll
-            for (int j = 0; j < kTok; ++j, y += C) {
-                h = advance(h, e1[j], u[j]);
-                if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C, even);
-            }
+            for (int j = 0; j < kTok; ++j) sm.held[warp][j][lane] = make_float4(e1[j].x, e1[j].y, u[j].x, u[j].y);
         }
     }
 }
@@ -772,7 +840,7 @@ struct BwdPlan {
         float4 part[kWarps][32];
         float2 rpart[kWarps][32];  // reverse sums
         float2 dA[2][kWarps][32];
-        Sync sync;
+        Sync<1> sync;
         static_assert(kStages + 2 <= kInfos, "a tile's place is taken while it is in use");
     };
     static constexpr int smem = kGroups * sizeof(Smem);
@@ -789,7 +857,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
     const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
     typename Plan::Smem &sm = reinterpret_cast<typename Plan::Smem *>(smem_raw)[group];
-    Sync &sync = sm.sync;
+    auto &sync = sm.sync;
     const int C = p.s.C;
     const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
     Tickets tickets(p.ws.ticket, p.tiles, kGroups, group);
@@ -800,8 +868,8 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         else t.tile = -1;
     };
     if (warp == kWarps && lane == 0) {
-        tc::mbar_init(&sync.parts, kWarps);
-        tc::mbar_init(&sync.ready, 1);
+        tc::mbar_init(&sync.parts[0], kWarps);
+        tc::mbar_init(&sync.ready[0], 1);
         tc::fence_mbar_init();
         for (int k = 0; k < NS + 1; ++k) set_tile(k, tickets.take());
     }
@@ -830,7 +898,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             float2 h = load2<VEC>(p.states + t.chunk * C + c, a0, a1), K = both(0.f);
             if (!t.last) K = get_state(p.ws, t.tile - int64_t(t.stride), lane);
             else if (p.dfin) K = load2<VEC>(p.dfin + int64_t(t.row) * C + c, a0, a1);
-            tc::mbar_wait(&sync.parts, k & 1, p.err);
+            tc::mbar_wait(&sync.parts[0], k & 1, p.err);
             float2 P = both(1.f), R = both(0.f);
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
@@ -840,7 +908,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             }
             if (!t.last && !__all_sync(0xffffffffu, set(K))) {
                 if (!t.first) put_sums(p.ws, t.tile, lane, P, R);
-                look_back(p.ws, t, lane, K, p.err);
+                look_back(p.ws, t, lane, K, p.err, [] {});
             }
             const float2 out = fma(P, K, R);
             if (!t.first) put_state(p.ws, t.tile, lane, out);
@@ -857,7 +925,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 reinterpret_cast<float2 *>(&sm.part[w][lane])[1] = K;
                 K = fma(q[w], K, sm.rpart[w][lane]);
             }
-            arrive_warp(&sync.ready, lane);
+            arrive_warp(&sync.ready[0], lane);
             if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
             if (k >= 1) sum_dA(k - 1);
             __syncwarp();
@@ -865,7 +933,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             __syncwarp();
         }
         if (k > 0) {  // the last tile: its warps say when they are through
-            tc::mbar_wait(&sync.parts, k & 1, p.err);
+            tc::mbar_wait(&sync.parts[0], k & 1, p.err);
             sum_dA(k - 1);
         }
         return;
@@ -960,8 +1028,8 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             sm.part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
             sm.rpart[warp][lane] = R;
         }
-        arrive_warp(&sync.parts, lane);
-        tc::mbar_wait(&sync.ready, k & 1, p.err);
+        arrive_warp(&sync.parts[0], lane);
+        tc::mbar_wait(&sync.ready[0], k & 1, p.err);
         const float4 s = sm.part[warp][lane];
         float2 K = make_float2(s.z, s.w), dA = both(0.f);
         {
@@ -1004,7 +1072,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         load(k + NS);
         A = rates(k + 1);
     }
-    arrive_warp(&sync.parts, lane);  // for the last tile's dA
+    arrive_warp(&sync.parts[0], lane);  // for the last tile's dA
 }
 
 // Column sums of a [rows, C] array: 32 columns a block, 32 rows at a time, each
