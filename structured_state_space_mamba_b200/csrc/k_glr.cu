@@ -586,8 +586,8 @@ struct FwdPlan {
     // A tile ahead: the gates of tile k + 1 are formed, and its sums published, while
     // tile k waits for its state; the terms of tile k stay in shared memory meanwhile.
     // Few chains need it: there a tile waits for the sums of several groups, and those
-    // used to wait for their own states first.  1 x 65536 x 2048 in bf16: 336 -> 270 us;
-    // 4 x 4096 x 5120: 140 -> 137.  In place of the second stage of copies; inputs in
+    // used to wait for their own states first.  1 x 65536 x 2048 in bf16: 336 -> 268 us;
+    // 4 x 4096 x 5120: 140 -> 138.  In place of the second stage of copies; inputs in
     // fp32 leave no room for the terms.
     static constexpr bool kHold = sizeof(T) == 2;
     static constexpr int kSlots = kHold ? 2 : 1;
@@ -760,15 +760,22 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     auto finish = [&](const Tile &t, const float4 (&part)[kWarps][32], auto term) {
         T *y = p.y + (t.base + (int64_t(warp * kTok) * C + 2 * lane));
         const bool even = C % 2 == 0;
-        const int c = t.ct * kGlrCols + 2 * lane, ntok = t.ntok - warp * kTok;
-        const bool full = t.full;
         float2 h = *reinterpret_cast<const float2 *>(&part[warp][lane]);
+        if (t.full) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j, y += C) {
-            const float4 q = term(j);
-            h = advance(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
-            if (full) store2<T, VEC>(y, h, true, true, even);
-            else if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C, even);
+            for (int j = 0; j < kTok; ++j, y += C) {
+                const float4 q = term(j);
+                h = advance(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
+                store2<T, VEC>(y, h, true, true, even);
+            }
+        } else {
+            const int c = t.ct * kGlrCols + 2 * lane, ntok = t.ntok - warp * kTok;
+#pragma unroll
+            for (int j = 0; j < kTok; ++j, y += C) {
+                const float4 q = term(j);
+                h = advance(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
+                if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C, even);
+            }
         }
     };
     load(0);
