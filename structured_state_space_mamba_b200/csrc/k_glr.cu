@@ -30,7 +30,8 @@
 // 144 us; 16 warps of four tokens: 162 us), nor an earlier hand-out of the states.
 // Backwards it is 150 instructions and 16 special functions a pair, about twice the
 // time.  With few chains (1 x 65536 x 2048: 32 of them for 444 groups) the tiles of
-// a chain wait for each other's sums through L2, three to four trips a tile: 330 us.
+// a chain wait for each other's sums through L2: 336 us, 268 us with the sums of a
+// tile formed ahead (hold_ahead).
 #include "common.cuh"
 #include "glr.h"
 #include "pack8.cuh"
@@ -532,10 +533,10 @@ struct Tickets {
 constexpr int kGroups = 3;
 constexpr int kBlock = kGroups * kGroupThreads;
 
-// The tiles of a group, in a ring: a tile is set before the starts of the last tile
-// but one before its copies begin are handed out, with which it becomes visible (tile
-// k + NS + 1 before those of tile k with NS stages).  No ticket is taken earlier than
-// that: a group that lags holds up the chains of all the tiles that it has taken.
+// The tiles of a group, in a ring: a tile's place is set before the starts of an
+// earlier one are handed out, with which it becomes visible, and that hand-out is
+// waited for before the tile's copies begin.  No ticket is taken earlier than that: a
+// group that lags holds up the chains of all the tiles that it has taken.
 constexpr int kInfos = 8;
 template <int SLOTS>
 struct Sync {
@@ -581,25 +582,19 @@ struct FwdArgs {
     int tiles;
     TileDivide dv;
 };
-template <typename T>
+template <typename T, bool HOLD>
 struct FwdPlan {
-    // A tile ahead: the gates of tile k + 1 are formed, and its sums published, while
-    // tile k waits for its state; the terms of tile k stay in shared memory meanwhile.
-    // Few chains need it: there a tile waits for the sums of several groups, and those
-    // used to wait for their own states first.  1 x 65536 x 2048 in bf16: 336 -> 268 us;
-    // 4 x 4096 x 5120: 140 -> 138.  In place of the second stage of copies; inputs in
-    // fp32 leave no room for the terms.
-    static constexpr bool kHold = sizeof(T) == 2;
-    static constexpr int kSlots = kHold ? 2 : 1;
-    static constexpr int kLead = kHold ? 3 : 2;  // tiles that are set before the first
+    static constexpr int kStages = sizeof(T) == 2 && !HOLD ? 2 : 1;
+    static constexpr int kSlots = HOLD ? 2 : 1;
+    static constexpr int kLead = HOLD ? 3 : kStages + 1;  // tiles that are set before the first
     struct Stage {
         T x[kWarpVals], r[kWarpVals], i[kWarpVals];
     };
     struct alignas(128) Smem {
-        Stage stage[kWarps];
+        Stage stage[kStages][kWarps];
         // products and sums of the warps' tokens; in their place then the states before them
         float4 part[kSlots][kWarps][32];
-        float4 held[kHold ? kWarps : 1][kHold ? kTok : 1][32];
+        float4 held[HOLD ? kWarps : 1][HOLD ? kTok : 1][32];
         Sync<kSlots> sync;
         static_assert(kLead + 2 <= kInfos, "a tile's place is taken while it is in use");
     };
@@ -607,11 +602,14 @@ struct FwdPlan {
     static_assert(smem <= 227 * 1024, "more shared memory than an SM has");
 };
 
-template <typename T, bool VEC, bool PACK>
+// HOLD: the gates of tile k + 1 are formed, and its sums published, while tile k
+// waits for its state; the terms of tile k stay in shared memory meanwhile, in
+// place of the second stage of copies (inputs in fp32 leave no room for them).
+template <typename T, bool VEC, bool PACK, bool HOLD>
 __global__ void __launch_bounds__(kBlock, 1)
 glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
-    using Plan = FwdPlan<T>;
-    constexpr int SL = Plan::kSlots, LEAD = Plan::kLead;
+    using Plan = FwdPlan<T, HOLD>;
+    constexpr int NS = Plan::kStages, SL = Plan::kSlots, LEAD = Plan::kLead;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const int group = threadIdx.x / kGroupThreads, lane = threadIdx.x & 31;
     const int warp = (threadIdx.x - group * kGroupThreads) >> 5;
@@ -691,7 +689,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     auto load = [&](int k) {
         const Tile &t = sync.tile[k & (kInfos - 1)];
         if (t.tile >= 0) {
-            typename Plan::Stage &st = sm.stage[warp];
+            typename Plan::Stage &st = sm.stage[k % NS][warp];
             T *const dst[3] = {st.x, st.r, st.i};
             const T *const src[3] = {p.x, p.r, p.i};
             fill<T, VEC, 3>(dst, src, t, C, warp, lane);
@@ -705,12 +703,12 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     };
     const Held hd;
     // the gates of a tile, and their product and sum
-    auto gates = [&](const Tile &t, float2 A, float2 (&e1)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32]) {
+    auto gates = [&](int k, const Tile &t, float2 A, float2 (&e1)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32]) {
         const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
-        copy_wait<0>();
+        copy_wait<NS - 1>();
         __syncwarp();
-        const typename Plan::Stage &st = sm.stage[warp];
+        const typename Plan::Stage &st = sm.stage[k % NS][warp];
         if (PACK) {
             const int64_t cols8 = (C + kPackBlock - 1) / kPackBlock;
             if constexpr (VEC) {
@@ -778,16 +776,16 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             }
         }
     };
-    load(0);
+    for (int k = 0; k < NS; ++k) load(k);
     float2 A = rates(0);
-    if constexpr (!Plan::kHold) {
+    if constexpr (!HOLD) {
         for (int k = 0;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
             float2 e1[kTok], u[kTok];
-            gates(t, A, e1, u, sm.part[0]);
+            gates(k, t, A, e1, u, sm.part[0]);
             arrive_warp(&sync.parts[0], lane);  // and this warp's part of the stage is read
-            load(k + 1);
+            load(k + NS);
             A = rates(k + 1);
             tc::mbar_wait(&sync.ready[0], k & 1, p.err);
             finish(t, sm.part[0], [&](int j) { return make_float4(e1[j].x, e1[j].y, u[j].x, u[j].y); });
@@ -799,7 +797,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             const bool more = n.tile >= 0;
             float2 e1[kTok], u[kTok];
             if (more) {
-                gates(n, A, e1, u, sm.part[(k + 1) % SL]);
+                gates(k + 1, n, A, e1, u, sm.part[(k + 1) % SL]);
                 arrive_warp(&sync.parts[(k + 1) % SL], lane);
                 load(k + 2);
                 A = rates(k + 2);
@@ -1154,6 +1152,17 @@ cudaError_t launch_tiles(K kernel, int smem, const GlrShape &s, A &a, cudaStream
     return cudaGetLastError();
 }
 
+// Whether a tile's gates are formed ahead of the state of the one before it.  With
+// few chains for the groups at work, the tiles of a chain wait for the sums of
+// several groups, and those for their own states first.  With many, nothing waits
+// long and the second stage of copies is worth more.  134 M values in bf16, us a
+// call ahead / not: 16 chains 409 / 475, 32 287 / 357, 64 275 / 300, 128 271 / 276,
+// 160 268 / 274, 256 267 / 267, 320 263 / 260, 640 262 / 253.
+bool hold_ahead(const GlrShape &s) {
+    const int64_t chains = int64_t(s.nct) * (s.nseq ? s.nseq : s.batch);
+    return 2 * chains <= int64_t(device_sm_count()) * kGroups;
+}
+
 template <typename T, bool VEC, bool PACK>
 cudaError_t forward_typed(const GlrShape &s, const void *x, const void *r, const void *i, const float *A,
                           const float *h0, void *y, float *fin, float *states, const GlrPacked *packed,
@@ -1164,7 +1173,10 @@ cudaError_t forward_typed(const GlrShape &s, const void *x, const void *r, const
     a.A = A; a.h0 = h0; a.y = static_cast<T *>(y); a.fin = fin; a.states = states;
     a.pk = packed ? *packed : GlrPacked{};
     a.err = err;
-    return launch_tiles(glr_forward_kernel<T, VEC, PACK>, FwdPlan<T>::smem, s, a, stream);
+    if constexpr (VEC && sizeof(T) == 2)  // rows off the vectors have no registers left for it
+        if (hold_ahead(s))
+            return launch_tiles(glr_forward_kernel<T, VEC, PACK, true>, FwdPlan<T, true>::smem, s, a, stream);
+    return launch_tiles(glr_forward_kernel<T, VEC, PACK, false>, FwdPlan<T, false>::smem, s, a, stream);
 }
 
 template <typename T, bool VEC, bool PACK>
