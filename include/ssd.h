@@ -474,7 +474,10 @@ SSD_API int64_t ssd_glr_chunk_rows(const ssd_glr_dims_t *dims, const int64_t *cu
  *   dy [B,T,C] dtype; dfinal_state [S, C] fp32 or NULL (zero)
  *   dx, dr, di [B,T,C] dtype (must not alias any input); dA [C] fp32;
  *   dinit_state [S, C] fp32 or NULL (an empty sequence's is its dfinal)
- * Scratch as for the forward pass.  dA is summed in a fixed order.
+ * Scratch as for the forward pass.  dA is summed in a fixed order.  Accuracy
+ * against the fp64 gradients (from checkpoints: of the values that they stand for):
+ * max abs error over max |value| <= 1e-5, plus half a step where bf16 is stored; for
+ * dA, whose terms may cancel, 1e-5 of the largest sum of its terms' magnitudes.
  */
 SSD_API ssd_status_t ssd_glr_backward(const ssd_glr_dims_t *dims, const int64_t *cu_seqlens, int64_t nseq,
                                       const void *x, const void *r, const void *i, const ssd_packed8_t *packed,
