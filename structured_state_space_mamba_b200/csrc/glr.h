@@ -33,7 +33,7 @@ struct GlrShape {
 // every pointer is null.
 struct GlrScratch {
     unsigned int *ticket;  // the last tile taken
-    float4 *sums;          // [tiles][32] products and sums of two channels a lane
+    float4 *sums;          // [tiles][32] decays and sums of two channels a lane
     float2 *state;         // [tiles][32] the state that leaves the tile
 };
 

@@ -7,10 +7,10 @@
 // and backwards in time, with K_t = dL/dh_{t-1} through the recurrence alone,
 //     G_t = dy_t + K_{t+1},  K_t = a_t G_t.
 //
-// Either is a scan of pairs (product of decays, sum): a tile of 64 tokens and 64
+// Either is a scan of pairs (decay, sum): a tile of 64 tokens and 64
 // channels is read once, its gates are formed in registers, and the tiles of
 // one chain (a sequence's chunks for 64 channels) hand the state on through
-// global memory in the same launch.  A tile publishes its (product, sum) as
+// global memory in the same launch.  A tile publishes its (decay, sum) as
 // soon as it has them; a later tile looks back over at most four predecessors
 // to the nearest one whose outgoing state is known and applies the sums in
 // between in their order, so the bits do not depend on how far it looked.
@@ -18,8 +18,10 @@
 // waits for one that a running block holds.
 //
 // A decay next to one, taken thousands of times, must not be rounded to a
-// multiple of 2^-24: everything works with e^l - 1, which keeps its own
-// relative precision (the recurrence is h + (e^l - 1) h + u).
+// multiple of 2^-24: a token works with e^l - 1, which keeps its own relative
+// precision (the recurrence is h + (e^l - 1) h + u), and the decay of several
+// tokens is the sum of their l until it is applied.  (As a product, it was off by
+// 1e-3 after 65536 tokens of constant gates, whose roundings all go one way.)
 //
 // What bounds it.  Compulsory traffic is 8 bytes a value forwards in bf16 and 14
 // backwards (11 from checkpoints).  On 4 x 4096 x 5120 the forward pass takes
@@ -135,13 +137,40 @@ __device__ __forceinline__ float2 decay_minus_1(float2 l, bool steep) {
     }
     return p;
 }
+// A decay e^l, l <= 0, as one number that keeps its own relative precision: e^l - 1 (at
+// most 0) from l = -1/2 up, e^l itself (positive, or -1 for 0) below.
+__device__ __forceinline__ float2 decay(float2 l) {
+    const bool steep = __any_sync(0xffffffffu, l.x < -0.5f || l.y < -0.5f);
+    float2 q = decay_minus_1(l, false);
+    if (steep) {
+        const float2 e = make_float2(ex2(l.x * kLog2e), ex2(l.y * kLog2e));
+        q.x = l.x < -0.5f ? (e.x == 0.f ? -1.f : e.x) : q.x;
+        q.y = l.y < -0.5f ? (e.y == 0.f ? -1.f : e.y) : q.y;
+    }
+    return q;
+}
+// The state behind tokens of that decay which add S themselves.
+__device__ __forceinline__ float2 behind(float2 h, float2 q, float2 S) {
+    return add(make_float2(q.x > 0.f ? 0.f : h.x, q.y > 0.f ? 0.f : h.y), fma(q, h, S));
+}
+// The sum of N numbers by pairs: exact where they are all the same.
+template <int N>
+__device__ __forceinline__ float2 sum_by_pairs(float2 (&v)[N]) {
+    static_assert((N & (N - 1)) == 0, "pairs of pairs");
+#pragma unroll
+    for (int o = 1; o < N; o *= 2)
+#pragma unroll
+        for (int w = 0; w < N; w += 2 * o) v[w] = add(v[w], v[w + o]);
+    return v[0];
+}
 // a^2 - 1 from a - 1
 __device__ __forceinline__ float2 square_minus_1(float2 e1) { return fma(e1, e1, add(e1, e1)); }
-// decay - 1 and what the token brings in, sqrt(1 - a^2) s(i) x, for r and i from -43 on
-__device__ __forceinline__ void token(const Held &hd, float2 x, float2 r, float2 i, float2 A, bool steep, float2 &e1,
-                                      float2 &u) {
+// l, decay - 1 and what the token brings in, sqrt(1 - a^2) s(i) x, for r and i from -43 on
+__device__ __forceinline__ void token(const Held &hd, float2 x, float2 r, float2 i, float2 A, bool steep, float2 &l,
+                                      float2 &e1, float2 &u) {
     const Sig g = sigmoids(hd, r, i);
-    e1 = decay_minus_1(mul(A, g.sr), steep);
+    l = mul(A, g.sr);
+    e1 = decay_minus_1(l, steep);
     const float2 w = square_minus_1(e1);
     u = mul(make_float2(root(-w.x), root(-w.y)), mul(g.si, x));
 }
@@ -343,9 +372,9 @@ __device__ __forceinline__ Tile decode_tile(const GlrShape &s, const TileDivide 
 // through L2.
 constexpr uint32_t kUnset = 0xffffffffu;
 
-__device__ __forceinline__ void put_sums(const GlrScratch &ws, int tile, int lane, float2 P, float2 S) {
+__device__ __forceinline__ void put_sums(const GlrScratch &ws, int tile, int lane, float2 q, float2 S) {
     asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(ws.sums + int64_t(tile) * 32 + lane),
-                 "f"(P.x), "f"(P.y), "f"(S.x), "f"(S.y) : "memory");
+                 "f"(q.x), "f"(q.y), "f"(S.x), "f"(S.y) : "memory");
 }
 __device__ __forceinline__ void put_state(const GlrScratch &ws, int tile, int lane, float2 h) {
     asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(ws.state + int64_t(tile) * 32 + lane),
@@ -404,7 +433,7 @@ __device__ __forceinline__ bool look_back(const GlrScratch &ws, const Tile &t, i
                 ok = true;
             } else if (d < kWindow - 1) {
                 ok = ok && set(sums[d]);
-                h = fma(make_float2(sums[d].x, sums[d].y), h, make_float2(sums[d].z, sums[d].w));
+                h = behind(h, make_float2(sums[d].x, sums[d].y), make_float2(sums[d].z, sums[d].w));
             }
         }
         if (__all_sync(0xffffffffu, ok)) return true;
@@ -520,7 +549,7 @@ struct Tickets {
 // a group: compute warps, which never wait for one another, and a scan warp
 // ---------------------------------------------------------------------------
 // Each compute warp copies, reads and writes its own eight tokens of every tile:
-// it forms their gates, leaves their product and sum, and finishes the tokens
+// it forms their gates, leaves their decay and sum, and finishes the tokens
 // once it has the state before them.  The scan warp takes the tickets, joins the
 // warps' sums, publishes them, looks back and hands every warp its start.  One
 // block an SM holds three such groups, which share nothing, so that two of them
@@ -550,16 +579,24 @@ __device__ __forceinline__ bool passed(uint64_t *bar, uint32_t parity) {
                  : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
     return __all_sync(0xffffffffu, ok != 0);
 }
-// the warps' products and sums, joined
-__device__ __forceinline__ void join(const float4 (&part)[kWarps][32], int lane, float2 &P, float2 &S) {
-    P = both(1.f);
-    S = both(0.f);
+// The decay of a tile from its warps' sums of l.  (Inside a tile the warps' decays are
+// plain numbers: a state passes eight of them at most, and the tile's own state
+// goes on from the one before it by this.)
+__device__ __forceinline__ float2 join_decay(const float2 (&ls)[kWarps][32], int lane) {
+    float2 l[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l[w] = ls[w][lane];
+    return decay(sum_by_pairs(l));
+}
+// its sum, from the warps' decays and sums
+__device__ __forceinline__ float2 join_sum(const float4 (&part)[kWarps][32], int lane) {
+    float2 S = both(0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        const float4 q = part[w][lane];
-        P = mul(P, make_float2(q.x, q.y));
-        S = fma(make_float2(q.x, q.y), S, make_float2(q.z, q.w));
+        const float4 v = part[w][lane];
+        S = fma(make_float2(v.x, v.y), S, make_float2(v.z, v.w));
     }
+    return S;
 }
 __device__ __forceinline__ void arrive_warp(uint64_t *bar, int lane) {
     __syncwarp();
@@ -592,8 +629,9 @@ struct FwdPlan {
     };
     struct alignas(128) Smem {
         Stage stage[kStages][kWarps];
-        // products and sums of the warps' tokens; in their place then the states before them
+        // decays and sums of the warps' tokens; in their place then the states before them
         float4 part[kSlots][kWarps][32];
+        float2 l[kSlots][kWarps][32];  // the decays' logarithms
         float4 held[HOLD ? kWarps : 1][HOLD ? kTok : 1][32];
         Sync<kSlots> sync;
         static_assert(kLead + 2 <= kInfos, "a tile's place is taken while it is in use");
@@ -635,7 +673,8 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
 
     if (warp == kWarps) {  // the scan warp
         uint32_t next = 0;  // a ticket taken a tile ago
-        bool published = false;  // this tile's sums, during the wait of the one before
+        bool published = false;  // this tile's decay and sum, during the wait of the one before
+        float2 q1 = both(0.f), S1 = both(0.f);
         if (lane == 0) next = tickets.take();
         for (int k = 0;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
@@ -649,10 +688,13 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             else if (p.h0) h = load2<VEC>(p.h0 + int64_t(t.row) * C + c, a0, a1);
             auto &part = sm.part[k % SL];
             tc::mbar_wait(&sync.parts[k % SL], (k / SL) & 1, p.err);
-            float2 P, S;
-            join(part, lane, P, S);
+            float2 q = q1, S = S1;
+            if (!published) {
+                q = join_decay(sm.l[k % SL], lane);
+                S = join_sum(part, lane);
+            }
             if (!t.first && !__all_sync(0xffffffffu, set(h))) {
-                if (!t.last && !published) put_sums(p.ws, t.tile, lane, P, S);
+                if (!t.last && !published) put_sums(p.ws, t.tile, lane, q, S);
                 published = false;
                 look_back(p.ws, t, lane, h, p.err, [&] {
                     if (SL == 1 || published) return;
@@ -660,22 +702,22 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
                     if (n.tile < 0 || n.first || n.last ||
                         !passed(&sync.parts[(k + 1) % SL], ((k + 1) / SL) & 1))
                         return;
-                    float2 P1, S1;
-                    join(sm.part[(k + 1) % SL], lane, P1, S1);
-                    put_sums(p.ws, n.tile, lane, P1, S1);
+                    q1 = join_decay(sm.l[(k + 1) % SL], lane);
+                    S1 = join_sum(sm.part[(k + 1) % SL], lane);
+                    put_sums(p.ws, n.tile, lane, q1, S1);
                     published = true;
                 });
             } else {
                 published = false;
             }
-            const float2 out = fma(P, h, S);
+            const float2 out = behind(h, q, S);
             if (!t.last) put_state(p.ws, t.tile, lane, out);
             const float2 start = h;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float4 q = part[w][lane];
+                const float4 v = part[w][lane];
                 *reinterpret_cast<float2 *>(&part[w][lane]) = h;
-                h = fma(make_float2(q.x, q.y), h, make_float2(q.z, q.w));
+                h = fma(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
             }
             arrive_warp(&sync.ready[k % SL], lane);
             if (p.states) store2<float, VEC>(p.states + t.chunk * C + c, start, a0, a1);
@@ -702,8 +744,9 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         return t.tile < 0 ? both(0.f) : load2<VEC>(p.A + c, c < C, c + 1 < C);
     };
     const Held hd;
-    // the gates of a tile, and their product and sum
-    auto gates = [&](int k, const Tile &t, float2 A, float2 (&e1)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32]) {
+    // the gates of a tile, and their decay and sum
+    auto gates = [&](int k, const Tile &t, float2 A, float2 (&e1)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32],
+                     float2 (&ls)[kWarps][32]) {
         const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
         copy_wait<NS - 1>();
@@ -736,23 +779,23 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
                 }
             }
         }
-        float2 P = both(1.f), S = both(0.f);
+        float2 l[kTok], S = both(0.f);
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
             const int o = j * kGlrCols + 2 * lane;
-            token(hd, unpack2(st.x + o), unpack2_at_least(st.r + o), unpack2_at_least(st.i + o), A, steep, e1[j], u[j]);
+            token(hd, unpack2(st.x + o), unpack2_at_least(st.r + o), unpack2_at_least(st.i + o), A, steep, l[j], e1[j],
+                  u[j]);
         }
         if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
             for (int j = 0; j < kTok; ++j)
-                if (j >= ntok) e1[j] = u[j] = both(0.f);
+                if (j >= ntok) l[j] = e1[j] = u[j] = both(0.f);
         }
+        const float2 L = sum_by_pairs(l);
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            P = fma(e1[j], P, P);
-            S = advance(S, e1[j], u[j]);
-        }
-        part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+        for (int j = 0; j < kTok; ++j) S = advance(S, e1[j], u[j]);
+        ls[warp][lane] = L;
+        part[warp][lane] = make_float4(ex2(L.x * kLog2e), ex2(L.y * kLog2e), S.x, S.y);
     };
     // a tile's tokens from the state before them; term(j): e^l - 1 and the input's part
     auto finish = [&](const Tile &t, const float4 (&part)[kWarps][32], auto term) {
@@ -783,7 +826,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
             float2 e1[kTok], u[kTok];
-            gates(k, t, A, e1, u, sm.part[0]);
+            gates(k, t, A, e1, u, sm.part[0], sm.l[0]);
             arrive_warp(&sync.parts[0], lane);  // and this warp's part of the stage is read
             load(k + NS);
             A = rates(k + 1);
@@ -797,7 +840,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             const bool more = n.tile >= 0;
             float2 e1[kTok], u[kTok];
             if (more) {
-                gates(k + 1, n, A, e1, u, sm.part[(k + 1) % SL]);
+                gates(k + 1, n, A, e1, u, sm.part[(k + 1) % SL], sm.l[(k + 1) % SL]);
                 arrive_warp(&sync.parts[(k + 1) % SL], lane);
                 load(k + 2);
                 A = rates(k + 2);
@@ -840,7 +883,7 @@ struct BwdPlan {
     };
     struct alignas(128) Smem {
         Stage stage[kStages][kWarps];
-        // products and forward sums; in their place then the state before the warp's
+        // l and forward sums; in their place then the state before the warp's
         // tokens and K behind them
         float4 part[kWarps][32];
         float2 rpart[kWarps][32];  // reverse sums
@@ -904,31 +947,31 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
             if (!t.last) K = get_state(p.ws, t.tile - int64_t(t.stride), lane);
             else if (p.dfin) K = load2<VEC>(p.dfin + int64_t(t.row) * C + c, a0, a1);
             tc::mbar_wait(&sync.parts[0], k & 1, p.err);
-            float2 P = both(1.f), R = both(0.f);
+            float2 l[kWarps], f[kWarps], R = both(0.f);
 #pragma unroll
-            for (int w = kWarps - 1; w >= 0; --w) {
-                const float2 q = *reinterpret_cast<const float2 *>(&sm.part[w][lane]);
-                P = mul(P, q);
-                R = fma(q, R, sm.rpart[w][lane]);
+            for (int w = 0; w < kWarps; ++w) {
+                l[w] = *reinterpret_cast<const float2 *>(&sm.part[w][lane]);
+                f[w] = make_float2(ex2(l[w].x * kLog2e), ex2(l[w].y * kLog2e));
             }
+            const float2 q = decay(sum_by_pairs(l));
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) R = fma(f[w], R, sm.rpart[w][lane]);
             if (!t.last && !__all_sync(0xffffffffu, set(K))) {
-                if (!t.first) put_sums(p.ws, t.tile, lane, P, R);
+                if (!t.first) put_sums(p.ws, t.tile, lane, q, R);
                 look_back(p.ws, t, lane, K, p.err, [] {});
             }
-            const float2 out = fma(P, K, R);
+            const float2 out = behind(K, q, R);
             if (!t.first) put_state(p.ws, t.tile, lane, out);
-            float2 q[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float4 v = sm.part[w][lane];
-                q[w] = make_float2(v.x, v.y);
                 *reinterpret_cast<float2 *>(&sm.part[w][lane]) = h;
-                h = fma(q[w], h, make_float2(v.z, v.w));
+                h = fma(f[w], h, make_float2(v.z, v.w));
             }
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
                 reinterpret_cast<float2 *>(&sm.part[w][lane])[1] = K;
-                K = fma(q[w], K, sm.rpart[w][lane]);
+                K = fma(f[w], K, sm.rpart[w][lane]);
             }
             arrive_warp(&sync.ready[0], lane);
             if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
@@ -1012,25 +1055,23 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         auto cotangent = [&](int j) -> float2 { return unpack2(st.dy + j * kGlrCols + 2 * lane); };
         float2 e1[kTok], u[kTok];
         {
-            float2 P = both(1.f), S = both(0.f), R = both(0.f);
+            float2 l[kTok], S = both(0.f), R = both(0.f);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) token(hd, input(0, j), gate(1, j), gate(2, j), A, steep, e1[j], u[j]);
+            for (int j = 0; j < kTok; ++j) token(hd, input(0, j), gate(1, j), gate(2, j), A, steep, l[j], e1[j], u[j]);
             if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
                 for (int j = 0; j < kTok; ++j)
-                    if (j >= ntok) e1[j] = u[j] = both(0.f);
+                    if (j >= ntok) l[j] = e1[j] = u[j] = both(0.f);
             }
+            const float2 L = sum_by_pairs(l);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                P = fma(e1[j], P, P);
-                S = advance(S, e1[j], u[j]);
-            }
+            for (int j = 0; j < kTok; ++j) S = advance(S, e1[j], u[j]);
 #pragma unroll
             for (int j = kTok - 1; j >= 0; --j) {
                 R = add(R, cotangent(j));  // 0 behind the end
                 R = fma(e1[j], R, R);
             }
-            sm.part[warp][lane] = make_float4(P.x, P.y, S.x, S.y);
+            sm.part[warp][lane] = make_float4(L.x, L.y, S.x, S.y);
             sm.rpart[warp][lane] = R;
         }
         arrive_warp(&sync.parts[0], lane);
@@ -1132,8 +1173,8 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
             iv = make_float2(to_f32<T>(i[o]), to_f32<T>(i[n]));
             h = make_float2(state[o], state[n]);
         }
-        float2 e1, u;
-        token(hd, xv, at_least(rv), at_least(iv), Av, true, e1, u);
+        float2 l, e1, u;
+        token(hd, xv, at_least(rv), at_least(iv), Av, true, l, e1, u);
         h = advance(h, e1, u);
         store2<float, VEC>(state + o, h, a0, a1);
         store2<T, VEC>(y + o, h, a0, a1);
