@@ -38,10 +38,10 @@ def s(v):
     return 1.0 / (1.0 + np.exp(-v))
 
 
-def problem(T):
+def problem(T, rates=RATES):
     """One channel for every pair of rates and inputs, i = 0.5 throughout: the numbers
     as the call sees them, in fp64 and on the device."""
-    rows = np.array([(*a, *b) for b in INPUTS for a in RATES], dtype=np.float32)
+    rows = np.array([(*a, *b) for b in INPUTS for a in rates], dtype=np.float32)
     A, r, x, h0, dy, df = (np.ascontiguousarray(c) for c in rows.T)
     i = np.full_like(A, 0.5)
     on = lambda v: torch.from_numpy(v).to(DEV)  # noqa: E731
@@ -85,4 +85,29 @@ def test_constant_gates(T):
         close(g[k][0], e[k], k)
     close(g["dinit_state"], e["dinit"][:1], "dinit")
     close(g["dA"][None], e["terms"].sum(axis=0)[None], "dA", np.abs(e["terms"]).sum(axis=0), values=T)
+    assert binding.device_status() == 0
+
+
+# a token's change far below a step of the state (2^-25 of it and less), for thousands of
+# tiles, and states that come to rest where what a tile adds is what it takes
+HELD = [(-2e-8, 30.0), (-1e-3, -33.0), (-1.7e-9, 30.0), (-6e-7, 1.0), (-1e-3, -20.0), (-1e-5, 30.0), (-1e-4, 30.0),
+        (-5e-6, 2.0)]
+
+
+@pytest.mark.parametrize("T", [65536, 1 << 20])
+def test_states_that_hardly_change(T):
+    """The changes of a tile add up, whatever a step of the state that they change."""
+    n, p = problem(T, HELD)
+    y, fin, saved = binding.glr_forward(p["x"], p["r"], p["i"], p["A"], init_state=p["h0"], return_final_state=True,
+                                        save="inputs")
+    g = binding.glr_backward(p["dy"], saved, dfinal_state=p["df"], return_dinit_state=True)
+    at = np.arange(0, T, 64)
+    e = exact(n, T, at)
+    close(y[0, ::64], e["y"], "y")
+    close(saved.chunk_states, e["before"], "chunk_states")
+    # (of the largest state: one that has decayed below 2^-126 rests on a multiple of 2^-149)
+    close(fin, exact(n, T, [T - 1])["y"], "final", np.abs(e["y"]).max(axis=0))
+    for k in ("dx", "dr", "di"):
+        close(g[k][0, ::64], e[k], k)
+    close(g["dinit_state"], e["dinit"][:1], "dinit", np.abs(e["dinit"]).max(axis=0))
     assert binding.device_status() == 0
