@@ -138,14 +138,15 @@ __device__ __forceinline__ float2 decay_minus_1(float2 l, bool steep) {
     return p;
 }
 // A decay e^l, l <= 0, as one number that keeps its own relative precision: e^l - 1 (at
-// most 0) from l = -1/2 up, e^l itself (positive, or -1 for 0) below.
+// most 0) from l = -1/2 up, e^l itself below, where it is positive: at least 2^-126, as
+// what it leaves of a state must not be a difference that is almost the state.
 __device__ __forceinline__ float2 decay(float2 l) {
     const bool steep = __any_sync(0xffffffffu, l.x < -0.5f || l.y < -0.5f);
     float2 q = decay_minus_1(l, false);
     if (steep) {
         const float2 e = make_float2(ex2(l.x * kLog2e), ex2(l.y * kLog2e));
-        q.x = l.x < -0.5f ? (e.x == 0.f ? -1.f : e.x) : q.x;
-        q.y = l.y < -0.5f ? (e.y == 0.f ? -1.f : e.y) : q.y;
+        q.x = l.x < -0.5f ? fmaxf(e.x, 0x1p-126f) : q.x;
+        q.y = l.y < -0.5f ? fmaxf(e.y, 0x1p-126f) : q.y;
     }
     return q;
 }
