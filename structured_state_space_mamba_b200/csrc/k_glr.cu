@@ -188,8 +188,8 @@ __device__ __forceinline__ void token(const Held &hd, float2 x, float2 r, float2
     const float2 w = square_minus_1(e1);
     u = mul(make_float2(root(-w.x), root(-w.y)), mul(g.si, x));
 }
-// 1 / sqrt(-w), 0 for 0
-__device__ __forceinline__ float inv_root(float w) { return w == 0.f ? 0.f : rsq(-w); }
+// 1 / sqrt(-w), 0 for 0 and for what the root takes as 0, numbers below the smallest normal one
+__device__ __forceinline__ float inv_root(float w) { return fabsf(w) < 0x1p-126f ? 0.f : rsq(-w); }
 // h + e1 h + u
 __device__ __forceinline__ float2 advance(float2 h, float2 e1, float2 u) { return add(fma(e1, h, h), u); }
 
