@@ -478,6 +478,9 @@ SSD_API int64_t ssd_glr_chunk_rows(const ssd_glr_dims_t *dims, const int64_t *cu
  * against the fp64 gradients (from checkpoints: of the values that they stand for):
  * max abs error over max |value| <= 1e-5, plus half a step where bf16 is stored; for
  * dA, whose terms may cancel, 1e-5 of the largest sum of its terms' magnitudes.
+ * (The states inside a chunk are formed again to 2^-24 of the state before each
+ * token: that shows in dr and dA only where such a state is all but gone at the
+ * next token and nothing has come in there.)
  */
 SSD_API ssd_status_t ssd_glr_backward(const ssd_glr_dims_t *dims, const int64_t *cu_seqlens, int64_t nseq,
                                       const void *x, const void *r, const void *i, const ssd_packed8_t *packed,

@@ -117,36 +117,32 @@ __device__ __forceinline__ Sig sigmoids(const Held &hd, float2 r, float2 i) {
     g.si = mul(dr, q);
     return g;
 }
-// Whether some decay of the warp's channels can fall below e^-1/2 (|l| <= |A|).
-__device__ __forceinline__ bool steep_warp(float2 A) {
-    return __any_sync(0xffffffffu, A.x < -0.5f || A.y < -0.5f);
-}
-// e^l - 1 for l <= 0.  From -1/2 up, l + l^2 q(l) with q the polynomial of degree 4
+// e^l - 1 for l from -1/2 to 0: l + l^2 p(l) with p the polynomial of degree 4
 // that meets (e^l - 1 - l) / l^2 at the five Chebyshev nodes of [-1/2, 0]: 1.3e-8
-// of the result off, at most.  Below, the exponential, whose error the
-// difference no longer magnifies.
-__device__ __forceinline__ float2 decay_minus_1(float2 l, bool steep) {
+// of the result off, at most.
+__device__ __forceinline__ float2 decay_minus_1(float2 l) {
     float2 p = make_float2(fmaf(l.x, 0.0011642870f, 0.0082382215f), fmaf(l.y, 0.0011642870f, 0.0082382215f));
     p = times_plus(l, p, 0.0416499302f);
     p = times_plus(l, p, 0.1666656286f);
     p = times_plus(l, p, 0.5f);
-    p = fma(mul(l, p), l, l);
-    if (steep) {
-        const float2 e = make_float2(ex2(l.x * kLog2e) - 1.f, ex2(l.y * kLog2e) - 1.f);
-        p = make_float2(l.x < -0.5f ? e.x : p.x, l.y < -0.5f ? e.y : p.y);
-    }
-    return p;
+    return fma(mul(l, p), l, l);
 }
-// A decay e^l, l <= 0, as one number that keeps its own relative precision: e^l - 1 (at
-// most 0) from l = -1/2 up, e^l itself below, where it is positive: at least 2^-126, as
-// what it leaves of a state must not be a difference that is almost the state.
+constexpr float kSteep = -0.5f;
+// Whether some decay of the warp's channels can be (|l| <= |A|).
+__device__ __forceinline__ bool steep_warp(float2 A) { return __any_sync(0xffffffffu, A.x < kSteep || A.y < kSteep); }
+// v below there, w from there on
+__device__ __forceinline__ float2 by_slope(float2 l, float2 v, float2 w) {
+    return make_float2(l.x < kSteep ? v.x : w.x, l.y < kSteep ? v.y : w.y);
+}
+__device__ __forceinline__ float2 decay_of(float2 l) { return make_float2(ex2(l.x * kLog2e), ex2(l.y * kLog2e)); }
+// The decay e^l of a tile as one number q that keeps its own relative precision: e^l - 1
+// (at most 0) from l = -1/2 up, e^l itself below, where it is positive: at least 2^-126,
+// as what it leaves of a state must not be a difference that is almost the state.
 __device__ __forceinline__ float2 decay(float2 l) {
-    const bool steep = __any_sync(0xffffffffu, l.x < -0.5f || l.y < -0.5f);
-    float2 q = decay_minus_1(l, false);
-    if (steep) {
-        const float2 e = make_float2(ex2(l.x * kLog2e), ex2(l.y * kLog2e));
-        q.x = l.x < -0.5f ? fmaxf(e.x, 0x1p-126f) : q.x;
-        q.y = l.y < -0.5f ? fmaxf(e.y, 0x1p-126f) : q.y;
+    float2 q = decay_minus_1(l);
+    if (__any_sync(0xffffffffu, l.x < kSteep || l.y < kSteep)) {
+        const float2 e = decay_of(l);
+        q = by_slope(l, make_float2(fmaxf(e.x, 0x1p-126f), fmaxf(e.y, 0x1p-126f)), q);
     }
     return q;
 }
@@ -179,19 +175,45 @@ __device__ __forceinline__ float2 sum_by_pairs(float2 (&v)[N]) {
 }
 // a^2 - 1 from a - 1
 __device__ __forceinline__ float2 square_minus_1(float2 e1) { return fma(e1, e1, add(e1, e1)); }
-// l, decay - 1 and what the token brings in, sqrt(1 - a^2) s(i) x, for r and i from -43 on
-__device__ __forceinline__ void token(const Held &hd, float2 x, float2 r, float2 i, float2 A, bool steep, float2 &l,
-                                      float2 &e1, float2 &u) {
+// h + e1 h + u
+__device__ __forceinline__ float2 advance(float2 h, float2 e1, float2 u) { return add(fma(e1, h, h), u); }
+// A token's decay.  Inside a tile the decay a itself does, as a state passes eight of
+// them at most (tiles go on from each other by the sum of l), but 1 - a^2 needs
+// e^l - 1 where a is next to one.
+struct Decay {
+    float2 e1;  // e^l - 1
+    float2 a;   // precise where e^l - 1 is no longer, below e^-1/2
+    float2 w;   // a^2 - 1
+};
+__device__ __forceinline__ Decay decay_of_token(const Held &hd, float2 l, bool steep) {
+    Decay d;
+    d.e1 = decay_minus_1(l);
+    d.a = add(d.e1, hd.one);
+    if (steep) {
+        const float2 e = decay_of(l);
+        d.e1 = by_slope(l, plus(e, -1.f), d.e1);
+        d.a = by_slope(l, e, d.a);
+    }
+    d.w = square_minus_1(d.e1);
+    return d;
+}
+// Calls f with a truth value as a type.
+template <typename F>
+__device__ __forceinline__ void by_path(bool v, F &&f) {
+    if (v) f(std::true_type{});
+    else f(std::false_type{});
+}
+// l, the decay and what the token brings in, sqrt(1 - a^2) s(i) x, for r and i from -43 on
+__device__ __forceinline__ Decay token(const Held &hd, float2 x, float2 r, float2 i, float2 A, bool steep, float2 &l,
+                                       float2 &u) {
     const Sig g = sigmoids(hd, r, i);
     l = mul(A, g.sr);
-    e1 = decay_minus_1(l, steep);
-    const float2 w = square_minus_1(e1);
-    u = mul(make_float2(root(-w.x), root(-w.y)), mul(g.si, x));
+    const Decay d = decay_of_token(hd, l, steep);
+    u = mul(make_float2(root(-d.w.x), root(-d.w.y)), mul(g.si, x));
+    return d;
 }
 // 1 / sqrt(-w), 0 for 0 and for what the root takes as 0, numbers below the smallest normal one
 __device__ __forceinline__ float inv_root(float w) { return fabsf(w) < 0x1p-126f ? 0.f : rsq(-w); }
-// h + e1 h + u
-__device__ __forceinline__ float2 advance(float2 h, float2 e1, float2 u) { return add(fma(e1, h, h), u); }
 
 // ---------------------------------------------------------------------------
 // storage: two channels a lane
@@ -763,9 +785,8 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
     };
     const Held hd;
     // the gates of a tile, and their decay and sum
-    auto gates = [&](int k, const Tile &t, float2 A, float2 (&e1)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32],
+    auto gates = [&](int k, const Tile &t, float2 A, float2 (&a)[kTok], float2 (&u)[kTok], float4 (&part)[kWarps][32],
                      float2 (&ls)[kWarps][32]) {
-        const bool steep = steep_warp(A);
         const int ntok = t.ntok - warp * kTok;  // of this warp's tokens
         copy_wait<NS - 1>();
         __syncwarp();
@@ -798,24 +819,30 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             }
         }
         float2 l[kTok], S = both(0.f);
+        by_path(steep_warp(A), [&](auto steep) {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            const int o = j * kGlrCols + 2 * lane;
-            token(hd, unpack2(st.x + o), unpack2_at_least(st.r + o), unpack2_at_least(st.i + o), A, steep, l[j], e1[j],
-                  u[j]);
-        }
+            for (int j = 0; j < kTok; ++j) {
+                const int o = j * kGlrCols + 2 * lane;
+                a[j] = token(hd, unpack2(st.x + o), unpack2_at_least(st.r + o), unpack2_at_least(st.i + o), A,
+                             decltype(steep)::value, l[j], u[j])
+                           .a;
+            }
+        });
         if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
             for (int j = 0; j < kTok; ++j)
-                if (j >= ntok) l[j] = e1[j] = u[j] = both(0.f);
+                if (j >= ntok) {
+                    l[j] = u[j] = both(0.f);
+                    a[j] = hd.one;
+                }
         }
-        const float2 L = sum_by_pairs(l);
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) S = advance(S, e1[j], u[j]);
+        for (int j = 0; j < kTok; ++j) S = fma(a[j], S, u[j]);
+        const float2 L = sum_by_pairs(l);
         ls[warp][lane] = L;
         part[warp][lane] = make_float4(ex2(L.x * kLog2e), ex2(L.y * kLog2e), S.x, S.y);
     };
-    // a tile's tokens from the state before them; term(j): e^l - 1 and the input's part
+    // a tile's tokens from the state before them; term(j): the decay and the input's part
     auto finish = [&](const Tile &t, const float4 (&part)[kWarps][32], auto term) {
         T *y = p.y + (t.base + (int64_t(warp * kTok) * C + 2 * lane));
         const bool even = C % 2 == 0;
@@ -823,16 +850,16 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         if (t.full) {
 #pragma unroll
             for (int j = 0; j < kTok; ++j, y += C) {
-                const float4 q = term(j);
-                h = advance(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
+                const float4 v = term(j);
+                h = fma(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
                 store2<T, VEC>(y, h, true, true, even);
             }
         } else {
             const int c = t.ct * kGlrCols + 2 * lane, ntok = t.ntok - warp * kTok;
 #pragma unroll
             for (int j = 0; j < kTok; ++j, y += C) {
-                const float4 q = term(j);
-                h = advance(h, make_float2(q.x, q.y), make_float2(q.z, q.w));
+                const float4 v = term(j);
+                h = fma(make_float2(v.x, v.y), h, make_float2(v.z, v.w));
                 if (j < ntok) store2<T, VEC>(y, h, c < C, c + 1 < C, even);
             }
         }
@@ -843,22 +870,22 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
         for (int k = 0;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             if (t.tile < 0) break;
-            float2 e1[kTok], u[kTok];
-            gates(k, t, A, e1, u, sm.part[0], sm.l[0]);
+            float2 a[kTok], u[kTok];
+            gates(k, t, A, a, u, sm.part[0], sm.l[0]);
             arrive_warp(&sync.parts[0], lane);  // and this warp's part of the stage is read
             load(k + NS);
             A = rates(k + 1);
             tc::mbar_wait(&sync.ready[0], k & 1, p.err);
-            finish(t, sm.part[0], [&](int j) { return make_float4(e1[j].x, e1[j].y, u[j].x, u[j].y); });
+            finish(t, sm.part[0], [&](int j) { return make_float4(a[j].x, a[j].y, u[j].x, u[j].y); });
         }
     } else {
         for (int k = -1;; ++k) {
             const Tile &t = sync.tile[k & (kInfos - 1)], &n = sync.tile[(k + 1) & (kInfos - 1)];
             if (k >= 0 && t.tile < 0) break;
             const bool more = n.tile >= 0;
-            float2 e1[kTok], u[kTok];
+            float2 a[kTok], u[kTok];
             if (more) {
-                gates(k + 1, n, A, e1, u, sm.part[(k + 1) % SL], sm.l[(k + 1) % SL]);
+                gates(k + 1, n, A, a, u, sm.part[(k + 1) % SL], sm.l[(k + 1) % SL]);
                 arrive_warp(&sync.parts[(k + 1) % SL], lane);
                 load(k + 2);
                 A = rates(k + 2);
@@ -869,7 +896,7 @@ glr_forward_kernel(const __grid_constant__ FwdArgs<T> p) {
             }
             if (!more) break;
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) sm.held[warp][j][lane] = make_float4(e1[j].x, e1[j].y, u[j].x, u[j].y);
+            for (int j = 0; j < kTok; ++j) sm.held[warp][j][lane] = make_float4(a[j].x, a[j].y, u[j].x, u[j].y);
         }
     }
 }
@@ -906,6 +933,7 @@ struct BwdPlan {
         float4 part[kWarps][32];
         float2 rpart[kWarps][32];  // reverse sums
         float2 dA[2][kWarps][32];
+        float2 before[2][32];  // K before the tile's tokens
         Sync<1> sync;
         static_assert(kStages + 2 <= kInfos, "a tile's place is taken while it is in use");
     };
@@ -942,7 +970,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
     __syncthreads();
 
     if (warp == kWarps) {  // the scan warp
-        // dA of tile k, which its warps have left by the time they leave the sums of tile k + 1
+        // dA and dinit of tile k, which its warps have left by the time they leave the sums of tile k + 1
         auto sum_dA = [&](int k) {
             const Tile &t = sync.tile[k & (kInfos - 1)];
             const int c = t.ct * kGlrCols + 2 * lane;
@@ -950,6 +978,9 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) sum = add(sum, sm.dA[k & 1][w][lane]);
             store2<float, VEC>(p.dA_part + t.chunk * C + c, sum, c < C, c + 1 < C);
+            // (the tile's own sums have decays far below one only as e^l - 1)
+            if (t.first && p.dinit)
+                store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, sm.before[k & 1][lane], c < C, c + 1 < C);
         };
         uint32_t next = 0;  // a ticket taken a tile ago
         if (lane == 0) next = tickets.take();
@@ -978,8 +1009,7 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 if (!t.first) put_sums(p.ws, t.tile, lane, q, R);
                 look_back(p.ws, t, lane, K, p.err, [] {});
             }
-            const float2 out = behind(K, q, R, shift_of(t.rank));
-            if (!t.first) put_state(p.ws, t.tile, lane, out);
+            if (!t.first) put_state(p.ws, t.tile, lane, behind(K, q, R, shift_of(t.rank)));
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float4 v = sm.part[w][lane];
@@ -992,7 +1022,6 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 K = fma(f[w], K, sm.rpart[w][lane]);
             }
             arrive_warp(&sync.ready[0], lane);
-            if (t.first && p.dinit) store2<float, VEC>(p.dinit + int64_t(t.row) * C + c, out, a0, a1);
             if (k >= 1) sum_dA(k - 1);
             __syncwarp();
             if (lane == 0) next = tickets.take();
@@ -1075,7 +1104,8 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
         {
             float2 l[kTok], S = both(0.f), R = both(0.f);
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) token(hd, input(0, j), gate(1, j), gate(2, j), A, steep, l[j], e1[j], u[j]);
+            for (int j = 0; j < kTok; ++j)
+                e1[j] = token(hd, input(0, j), gate(1, j), gate(2, j), A, steep, l[j], u[j]).e1;
             if (ntok < kTok) {  // behind the sequence's end: the identity
 #pragma unroll
                 for (int j = 0; j < kTok; ++j)
@@ -1115,23 +1145,26 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
                 if (!all && j >= ntok) continue;
                 const Sig sg = sigmoids(hd, gate(1, j), gate(2, j));
                 const float2 sr = sg.sr, si = sg.si, er = sg.er, ei = sg.ei;
-                const float2 w = square_minus_1(e1[j]), rs = make_float2(inv_root(w.x), inv_root(w.y));
-                const float2 m = mul(make_float2(-w.x, -w.y), rs), a = plus(e1[j], 1.f), six = mul(si, input(0, j));
+                const float2 w = square_minus_1(e1[j]);
+                const float2 l = mul(A, sr), a = decay_of(l);
+                const float2 rs = make_float2(inv_root(w.x), inv_root(w.y)), m = mul(make_float2(-w.x, -w.y), rs);
+                const float2 six = mul(si, input(0, j));
                 const float2 G = add(K, cotangent(j)), Gm = mul(G, m);
                 // (G (h_t - s(i) x / m) would do, as a^2 + m^2 = 1, but for a small a it is
                 // the difference of two numbers that are almost the same)
                 const float2 as = mul(mul(a, six), rs);
                 const float2 dl = mul(mul(G, a), add(u[j], make_float2(-as.x, -as.y)));
                 dA = fma(dl, sr, dA);
-                K = fma(e1[j], G, G);
+                K = mul(a, G);
                 store2<T, VEC>(p.dx + o, mul(Gm, si), all || a0, all || a1, even);
                 store2<T, VEC>(p.di + o, mul(mul(Gm, six), mul(ei, si)), all || a0, all || a1, even);
-                store2<T, VEC>(p.dr + o, mul(mul(dl, mul(A, sr)), mul(er, sr)), all || a0, all || a1, even);
+                store2<T, VEC>(p.dr + o, mul(mul(dl, l), mul(er, sr)), all || a0, all || a1, even);
             }
         };
         if (t.full) walk(true);
         else walk(false);
         sm.dA[k & 1][warp][lane] = dA;
+        if (warp == 0) sm.before[k & 1][lane] = K;
         __syncwarp();  // this warp's part of the stage is read
         load(k + NS);
         A = rates(k + 1);
@@ -1191,9 +1224,10 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
             iv = make_float2(to_f32<T>(i[o]), to_f32<T>(i[n]));
             h = make_float2(state[o], state[n]);
         }
-        float2 l, e1, u;
-        token(hd, xv, at_least(rv), at_least(iv), Av, true, l, e1, u);
-        h = advance(h, e1, u);
+        // one token after another goes on from what this leaves, so e^l - 1 where it is precise
+        float2 l, u;
+        const Decay d = token(hd, xv, at_least(rv), at_least(iv), Av, true, l, u);
+        h = add(by_slope(l, mul(d.a, h), fma(d.e1, h, h)), u);
         store2<float, VEC>(state + o, h, a0, a1);
         store2<T, VEC>(y + o, h, a0, a1);
     }

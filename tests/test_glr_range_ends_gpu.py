@@ -105,3 +105,95 @@ def test_rates_below_the_normal_numbers(oracle, T, save):
             terms = np.abs(G * v[3] * gate * (1 - gate)) * (np.abs(a * kept) + np.abs(a * a * inp * v[0] / m))
         off = np.abs(host(g["dr"]) - gr["dr"])
         assert (off[0, :, 6:].max(axis=0) <= 1e-5 * terms[0, :, 6:].max(axis=0)).all()
+
+
+# tokens and the logarithm of all of their decays together
+LENGTHS = [(1, 20.0), (1, 15.0), (1, 10.0), (1, 0.7), (2, 20.0), (3, 20.0), (9, 20.0), (17, 20.0), (70, 20.0),
+           (70, 3.0), (200, 20.0), (1000, 20.0), (1000, 2.0)]
+
+
+def vanishing(T, total):
+    """Every token's decay e^(-total / T), by gates at different places; no input, so that
+    nothing but what is left of the state (and of its cotangent) comes out."""
+    r = np.array([0.0, 1.0, -1.0, 3.0, -4.0, 30.0, 0.5, -7.0], dtype=np.float32)
+    A = (-total / T * (1 + np.exp(-r.astype(np.float64)))).astype(np.float32)
+    rng = np.random.default_rng(T)
+    h0, df = rng.standard_normal((2, 1, 8)).astype(np.float32)
+    wide = lambda v: np.broadcast_to(v, (1, T, 8)).astype(np.float32)  # noqa: E731
+    return A, wide(r), wide(0.5), wide(0.0), wide(0.0), h0, df
+
+
+@pytest.mark.parametrize("T,total", LENGTHS)
+def test_what_is_left_of_a_state(oracle, T, total):
+    A, r, i, x, dy, h0, df = vanishing(T, total)
+    v = [np.asarray(t, dtype=np.float64) for t in (x, r, i, A)]
+    y, fin, saved = binding.glr_forward(on(x), on(r), on(i), on(A), init_state=on(h0), return_final_state=True,
+                                        save="inputs")
+    g = binding.glr_backward(on(dy), saved, dfinal_state=on(df), return_dinit_state=True)
+    yr, fr, _ = oracle.glr(*v, h0)
+    close(y, yr, "y")
+    close(fin, fr, "final")
+    gr = oracle.glr_grad(*v, dy.astype(np.float64), h0, df)
+    close(g["dinit_state"], gr["dh0"], "dinit")
+    # the reference's 1 - s(r) keeps 2^-53 of one only, 1e-3 of itself at r = 30; s(-r) is the same
+    gate = 1 / (1 + np.exp(-v[1]))
+    # the states that the backward pass forms again have a as 1 + (a - 1), off by 2^-25 of one:
+    # that of the state before, or 2^-25 / a of what is left of it,
+    # at every token, and 2^-25 once more for the product's own rounding
+    rel = 1e-5 + (T - 1) * 2.0 ** -24 * np.exp(total / T)
+    close(g["dr"], gr["dr"] / (1 - gate) * (gate * np.exp(-v[1])), "dr", rel)
+    close(g["dA"][None], gr["dA"][None], "dA", rel)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("total", [0.3, 0.7, 5.0, 10.0, 15.0, 20.0])
+def test_step_keeps_what_is_left_of_a_state(oracle, total, dtype):
+    t = dict(bf16=torch.bfloat16, f32=torch.float32)[dtype]
+    A, r, i, x, _, h0, _ = vanishing(1, total)
+    r = host(on(r, t))
+    state = on(h0)
+    y = binding.glr_step(state, on(x[:, 0], t), on(r[:, 0], t), on(i[:, 0], t), on(A))
+    _, fr, _ = oracle.glr(x, r, i, A, h0)
+    close(state, fr, "state")
+    close(y, fr, "y", rel=1e-5 + (2.0 ** -8 if dtype == "bf16" else 0.0))
+
+
+def test_steep_and_flat_channels_side_by_side(oracle):
+    """Decays from 1 - 1e-6 to e^-12 among the 64 channels of a tile, inputs and
+    cotangents everywhere, in whole tiles and ragged ones."""
+    B, T, C = 1, 333, 100
+    rng = np.random.default_rng(5)
+    A = -np.exp(np.linspace(np.log(1e-6), np.log(20.0), C)).astype(np.float32)
+    rng.shuffle(A)
+    x, r, i, dy = (rng.standard_normal((B, T, C)).astype(np.float32) for _ in range(4))
+    h0, df = rng.standard_normal((2, B, C)).astype(np.float32)
+    y, fin, saved = binding.glr_forward(on(x), on(r), on(i), on(A), init_state=on(h0), return_final_state=True,
+                                        save="inputs")
+    g = binding.glr_backward(on(dy), saved, dfinal_state=on(df), return_dinit_state=True)
+    v = [np.asarray(t, dtype=np.float64) for t in (x, r, i, A)]
+    yr, fr, _ = oracle.glr(*v, h0)
+    gr = oracle.glr_grad(*v, dy.astype(np.float64), h0, df)
+    close(y, yr, "y")
+    assert np.abs(host(fin) - fr).max() <= 1e-5 * np.abs(yr).max()
+    for k in ("dx", "dr", "di"):
+        close(g[k], gr[k], k)
+    assert np.abs(host(g["dinit_state"]) - gr["dh0"]).max() <= 1e-5 * np.abs(gr["dh0"]).max()
+
+
+@pytest.mark.parametrize("neighbour", [-0.1, -30.0])
+@pytest.mark.parametrize("rate", [1e-6, 0.3, 5.0])
+def test_a_positive_rate_is_a_nan(rate, neighbour):
+    """Whatever the rates beside it, forwards, backwards and in a step."""
+    T, C = 70, 16
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(1)
+    x, r, i, dy = torch.randn(4, 1, T, C, generator=gen, device=DEV)
+    A = torch.full((C,), neighbour, device=DEV)
+    A[3] = rate
+    others = [c for c in range(C) if c != 3]
+    y, fin, saved = binding.glr_forward(x, r, i, A, return_final_state=True, save="inputs")
+    g = binding.glr_backward(dy, saved)
+    state = torch.zeros(1, C, device=DEV)
+    binding.glr_step(state, *(t[:, 0].contiguous() for t in (x, r, i)), A)
+    for t in (y, fin, state, g["dx"], g["dr"], g["di"], g["dA"]):
+        assert torch.isnan(t[..., 3]).all() and torch.isfinite(t[..., others]).all()
