@@ -1173,15 +1173,22 @@ glr_backward_kernel(const __grid_constant__ BwdArgs<T> p) {
 }
 
 // Column sums of a [rows, C] array: 32 columns a block, 32 rows at a time, each
-// thread in order and then the 32 partial sums in order.
+// thread in order and then the 32 partial sums in order.  A thread of a long
+// sequence adds thousands of terms of one sign, so it keeps what each addition
+// rounds away (1e-4 of the sum without, 2^24 tokens).
 __global__ void __launch_bounds__(1024)
 row_sum_kernel(const float *__restrict__ part, int64_t rows, int C, float *__restrict__ out) {
     __shared__ float acc[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
-    float s = 0.f;
+    float s = 0.f, lost = 0.f;
     if (c < C)
-        for (int64_t r = threadIdx.y; r < rows; r += 32) s += __ldg(part + r * C + c);
-    acc[threadIdx.y][threadIdx.x] = s;
+#pragma unroll 4
+        for (int64_t r = threadIdx.y; r < rows; r += 32) {
+            const float v = __ldg(part + r * C + c), t = s + v, of_v = t - s;
+            lost += (s - (t - of_v)) + (v - of_v);
+            s = t;
+        }
+    acc[threadIdx.y][threadIdx.x] = isfinite(lost) ? s + lost : s;  // an infinite sum stays one
     __syncthreads();
     if (threadIdx.y == 0 && c < C) {
         float t = 0.f;

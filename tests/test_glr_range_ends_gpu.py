@@ -197,3 +197,25 @@ def test_a_positive_rate_is_a_nan(rate, neighbour):
     binding.glr_step(state, *(t[:, 0].contiguous() for t in (x, r, i)), A)
     for t in (y, fin, state, g["dx"], g["dr"], g["di"], g["dA"]):
         assert torch.isnan(t[..., 3]).all() and torch.isfinite(t[..., others]).all()
+
+
+def test_sum_of_a_rate_over_a_long_sequence():
+    """dA over 2^24 tokens whose terms are all of one sign and all but the same."""
+    T, C = 1 << 24, 8
+    one = torch.ones(1, T, C, device=DEV)
+    A = on(np.linspace(-0.5, -0.05, C))
+    y, saved = binding.glr_forward(one, 0 * one, one, A, save="inputs")
+    dA = host(binding.glr_backward(one, saved)["dA"])
+    # steady from a few hundred tokens on: h = u / (1 - a), G = dy / (1 - a); the first and
+    # the last of them are a share of 1e-4 of the sum at most and are added one by one
+    a, si = np.exp(host(A) / 2), 1 / (1 + np.exp(-1.0))
+    u = np.sqrt(1 - a * a) * si
+    edge = 2000
+    t = np.arange(edge, dtype=np.float64)[:, None]
+    h, G = u / (1 - a), 1 / (1 - a)
+    rest = a * a * si / np.sqrt(1 - a * a)
+    dl = G * (a * h - rest)
+    first = G * (a * (h * (1 - a ** t)) - rest)
+    last = G * (1 - a ** (t + 1)) * (a * h - rest)
+    want = 0.5 * ((T - 2 * edge) * dl + first.sum(axis=0) + last.sum(axis=0))
+    assert (np.abs(dA - want) <= 1e-5 * np.abs(want)).all(), dA / want - 1
