@@ -1218,8 +1218,8 @@ glr_step_kernel(int batch, int C, const T *__restrict__ x, const T *__restrict__
     if (!a0) return;
     const float2 Av = load2<VEC>(A + c, a0, a1);
     const Held hd;
-    for (int b = blockIdx.y; b < batch; b += gridDim.y) {
-        const int64_t o = int64_t(b) * C + c;
+    for (int64_t b = blockIdx.y; b < batch; b += gridDim.y) {  // up to 2^31 - 1 rows: the next index may be past them
+        const int64_t o = b * C + c;
         float2 xv, rv, iv, h;
         if (VEC) {
             xv = unpack2(x + o); rv = unpack2(r + o); iv = unpack2(i + o);
