@@ -571,15 +571,15 @@ __device__ __forceinline__ void fill(T *const (&dst)[N], const T *const (&src)[N
 // Tiles by ticket, or strided over the grid where no state is handed on.
 struct Tickets {
     unsigned int *ticket;
-    int tiles, mine, step;
+    uint32_t tiles, mine, step;  // tiles < 2^31, so that a step past them is a number still
     __device__ __forceinline__ Tickets(unsigned int *t, int n, int groups, int group)
         : ticket(t), tiles(n), mine(group * gridDim.x + blockIdx.x), step(groups * gridDim.x) {}
     // The next tile, raw: what atomicAdd returned, whose first use waits for it.
     __device__ __forceinline__ uint32_t take() {
         if (ticket) return atomicAdd(ticket, 1u);
-        const int n = mine;
+        const uint32_t n = mine;
         mine = mine > tiles ? mine : mine + step;
-        return uint32_t(n) - 1u;
+        return n - 1u;
     }
     // The ticket word starts at all ones, so a raw ticket is one less than its tile.
     static __device__ __forceinline__ int tile_of(uint32_t raw) { return int(min(raw + 1u, 0x7fffffffu)); }
