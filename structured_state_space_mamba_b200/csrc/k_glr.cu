@@ -359,8 +359,9 @@ struct TileDivide {
     Divide nct, batch;
 };
 
-// Tickets run over the channel tiles fastest, then over the chains, then along
-// them (against time for the backward pass).
+// Tickets run over the channel tiles fastest, then over a batch's rows, then along
+// them (against time for the backward pass); packed sequences come one after another,
+// each along its chunks.
 __device__ __forceinline__ Tile decode_tile(const GlrShape &s, const TileDivide &dv, int tile, bool reverse) {
     Tile t;
     t.tile = tile;
@@ -1255,12 +1256,23 @@ cudaError_t launch_tiles(K kernel, int smem, const GlrShape &s, A &a, cudaStream
 // Whether a tile's gates are formed ahead of the state of the one before it.  With
 // few chains for the groups at work, the tiles of a chain wait for the sums of
 // several groups, and those for their own states first.  With many, nothing waits
-// long and the second stage of copies is worth more.  134 M values in bf16, us a
-// call ahead / not: 16 chains 409 / 475, 32 287 / 357, 64 275 / 300, 128 271 / 276,
-// 160 268 / 274, 256 267 / 267, 320 263 / 260, 640 262 / 253.
+// long and the second stage of copies is worth more.  What counts are the chains that
+// are in flight together: all of a batch's, whose tickets go round them chunk by
+// chunk, but of packed sequences, which come one after another, the channel tiles
+// of one, or as many sequences' as the groups hold at a time.  134 M values in
+// bf16, us a call ahead / not.  Batches: 16 chains 409 / 475, 32 287 / 357, 64 275 / 300,
+// 128 271 / 276, 160 268 / 274, 256 267 / 267, 320 263 / 260, 640 262 / 253.  Packed, 2048
+// channels: 1 sequence 291 / 340, 16 299 / 374, 160 397 / 560; 5120: 16 258 / 283, 160
+// 303 / 366; 10240: 16 239 / 244, 160 of 2 chunks each 338 / 335.
 bool hold_ahead(const GlrShape &s) {
-    const int64_t chains = int64_t(s.nct) * (s.nseq ? s.nseq : s.batch);
-    return 2 * chains <= int64_t(device_sm_count()) * kGroups;
+    const int64_t groups = int64_t(device_sm_count()) * kGroups;
+    int64_t chains = int64_t(s.nct) * (s.nseq ? s.nseq : s.batch);
+    if (s.nseq) {
+        const int64_t held = groups * s.nseq / s.nc;  // by the mean length
+        const int64_t together = held > s.nct ? held : s.nct;
+        if (together < chains) chains = together;
+    }
+    return 2 * chains <= groups;
 }
 
 template <typename T, bool VEC, bool PACK>
