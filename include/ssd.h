@@ -508,8 +508,9 @@ SSD_API ssd_status_t ssd_glr_step(const ssd_glr_dims_t *dims, const void *x_t, c
  *     (o_p, o_q) = (n_p cos - n_q sin, n_p sin + n_q cos),  angle = pos * inv_freq_j
  *
  * for the pairs j < rotary / 2: (p, q) = (j, j + rotary / 2), or (2j, 2j + 1)
- * with `interleaved`; values from `rotary` on are normed only.  The angle is
- * formed in 64 bits (positions may be far), once a token for all groups.
+ * with `interleaved`; values from `rotary` on are normed only.  Positions may be
+ * far: a position's turns are formed in twice 64 bits, once a token for all
+ * groups, and their fraction is rounded to 2^-25 of a turn.
  *
  *   Bm, Cm      [B, T, G, N] dtype; a token's G * N values are contiguous, the
  *               strides between tokens and between batch rows are given (in

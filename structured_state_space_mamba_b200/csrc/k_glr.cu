@@ -1260,10 +1260,11 @@ cudaError_t launch_tiles(K kernel, int smem, const GlrShape &s, A &a, cudaStream
 // are in flight together: all of a batch's, whose tickets go round them chunk by
 // chunk, but of packed sequences, which come one after another, the channel tiles
 // of one, or as many sequences' as the groups hold at a time.  134 M values in
-// bf16, us a call ahead / not.  Batches: 16 chains 409 / 475, 32 287 / 357, 64 275 / 300,
-// 128 271 / 276, 160 268 / 274, 256 267 / 267, 320 263 / 260, 640 262 / 253.  Packed, 2048
-// channels: 1 sequence 291 / 340, 16 299 / 374, 160 397 / 560; 5120: 16 258 / 283, 160
-// 303 / 366; 10240: 16 239 / 244, 160 of 2 chunks each 338 / 335.
+// bf16, us on the device ahead / not.  Batches: 16 chains 450 / 480, 32 289 / 338,
+// 64 254 / 283, 128 238 / 248, 160 233 / 242, 256 224 / 230, 320 224 / 228, 640 222 / 220 (the
+// border is on the safe side).  Packed, 2048 channels: 1 sequence 291 / 340, 16 299 /
+// 374, 160 397 / 560; 5120: 16 258 / 283, 160 303 / 366; 10240: 16 239 / 244, 160 of 2
+// chunks each 338 / 335.
 bool hold_ahead(const GlrShape &s) {
     const int64_t groups = int64_t(device_sm_count()) * kGroups;
     int64_t chains = int64_t(s.nct) * (s.nseq ? s.nseq : s.batch);

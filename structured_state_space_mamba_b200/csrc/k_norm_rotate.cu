@@ -13,7 +13,7 @@
 // pairs: nothing but the sums crosses lanes.  The lane forms its four angles
 // once and walks the token's groups, B and C side by side, so that sines and
 // cosines cost 1 / (2 G) of what they would a row.  Positions may be far: the
-// angle is a 64-bit number of turns, and only its fraction becomes fp32.
+// turns are two 64-bit numbers, and only their fraction becomes fp32.
 //
 // 65536 tokens x 8 groups x 128, bf16, slices of a projection: 93 us on the device,
 // 5.8 TB/s (125 us with scalar arithmetic and a load at a time; 101 us with six blocks
@@ -30,8 +30,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// blocks an SM holds (seven cost the bf16 kernel up to 24 spilled bytes outside its
-// inner loop, and it is the faster for the loads that they have in flight)
+// blocks an SM holds (seven cost the bf16 kernel off the wide vectors 12 spilled bytes
+// outside its inner loop, and it is the faster for the loads that they have in flight)
 template <typename T> constexpr int kForwardPerSm = sizeof(T) == 2 ? 7 : 5;
 constexpr int kBackwardPerSm = 4;
 constexpr int kAnyPerSm = 8;
@@ -90,11 +90,18 @@ __device__ __forceinline__ void sincos_turn(float f, float &s, float &c) {
     }
 }
 
-// turns of a position: the fraction, rounded once to fp32
-constexpr double kInvTwoPi = 0.15915494309189533577;
+// Turns of a position: the fraction, rounded once to fp32.  A position may have 53 bits
+// and as many turns before the point, so both products, freq / (2 pi) and that times the
+// position, are formed in two doubles each; what is left out is below 2^-50 of a turn.
+// (In one double, an angle was off by 1e-4 at 2^40 and by anything at 2^53.)
+constexpr double kInvTwoPi = 0x1.45f306dc9c883p-3, kInvTwoPiLow = -0x1.6b01ec5417056p-57;
 __device__ __forceinline__ float turn_fraction(double pos, float freq) {
-    const double t = pos * (double(freq) * kInvTwoPi);
-    return float(t - rint(t));
+    asm volatile("" : "+f"(freq));  // both products again for every token, not in registers across them
+    const double f = double(freq), hi = f * kInvTwoPi;
+    const double lo = __fma_rn(f, kInvTwoPiLow, __fma_rn(f, kInvTwoPi, -hi));
+    const double t = pos * hi, rest = __fma_rn(pos, lo, __fma_rn(pos, hi, -t));
+    const double turn = (t - rint(t)) + rest;
+    return float(turn - rint(turn));
 }
 
 // A lane's eight values, v[0 .. 3] in pairs of neighbours: where they lie, and how
