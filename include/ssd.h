@@ -358,12 +358,15 @@ SSD_API ssd_status_t ssd_backward(const ssd_dims_t *dims, const void *x, const f
  *
  * A is the per-channel decay rate (A_c <= 0, as A of ssd_forward is; a channel
  * with A_c > 0 comes out as NaN).  Sizes: any batch, seqlen, channels >= 1
- * (no alignment of any of them) with seqlen <= 2^30, channels <= 2^24 and
+ * (sizes need no alignment; tensors are contiguous on 16 bytes as elsewhere) with
+ * seqlen <= 2^30, channels <= 2^24 and
  * fewer than 2^31 tiles of 64 channels and SSD_GLR_CHUNK tokens (else
  * SSD_ERR_UNSUPPORTED); dtype is the storage type of x, r, i, y and their
  * gradients, A, states and dA are fp32.  States and sums are held in fp32;
- * every pass gives the same bits for the same inputs, however a batch is cut
- * into calls.  Gates saturate at s(-43) = 2e-19.  A NaN or an infinity stays in
+ * every pass gives the same bits for the same inputs, however the rows of a batch
+ * are cut into calls (a sequence cut in time goes on from a state rounded to fp32).
+ * Gates saturate at s(-43) = 2e-19, and 1 - a_t^2 below 2^-126 counts as 0.  A NaN
+ * or an infinity stays in
  * its channel of its sequence: before its token nothing changes, from it on the
  * states are NaN or infinite.  Tiles of one call wait for each other on the device,
  * with a limit (ssd_device_status).
@@ -413,7 +416,9 @@ SSD_API ssd_status_t ssd_unpack8(int64_t rows, int64_t cols, int dtype, const ss
  * (`packed`: three, in that order) in place of the tensors themselves: x as
  * rows of headdim values (B T H of them), Bm and Cm as rows of dstate values (B T G).
  * The gradients at the values that the checkpoints stand for; everything else as
- * for ssd_backward, with dims->dtype the type of dy and of dx, dB, dC.
+ * for ssd_backward, with dims->dtype the type of dy and of dx, dB, dC.  The three are
+ * read back into scratch of that type first, so that what they save between the two
+ * passes is taken again while this one runs.
  */
 SSD_API ssd_status_t ssd_backward_packed8(const ssd_dims_t *dims, const ssd_packed8_t *packed, const float *dt,
                                           const float *A, const float *D, int chunk_len,
@@ -441,8 +446,9 @@ SSD_API ssd_status_t ssd_backward_packed8(const ssd_dims_t *dims, const ssd_pack
  *               ssd_glr_backward takes it
  *   packed_out  NULL, or three ssd_packed8_t that receive the 8-bit
  *               checkpoints of x, r and i (rows = B T, cols = C)
- * One kernel per 160 sequences (one for any batch); scratch for the hand-off
- * between tiles (about 0.1 byte a value) is allocated stream-ordered on
+ * One kernel per 160 sequences (one for any batch).  Where some sequence is longer
+ * than a chunk, scratch for the hand-off between tiles (768 bytes for every 64
+ * channels, or part of them, of every chunk) is allocated stream-ordered on
  * `stream` from the library's workspace pool and released to it before
  * return.  Accuracy against the fp64 recurrence: max|h - h_ref| / max|h_ref|
  * <= 1e-5 for states and SSD_F32, <= 2^-8 for y in SSD_BF16.
@@ -474,7 +480,8 @@ SSD_API int64_t ssd_glr_chunk_rows(const ssd_glr_dims_t *dims, const int64_t *cu
  *   dy [B,T,C] dtype; dfinal_state [S, C] fp32 or NULL (zero)
  *   dx, dr, di [B,T,C] dtype (must not alias any input); dA [C] fp32;
  *   dinit_state [S, C] fp32 or NULL (an empty sequence's is its dfinal)
- * Scratch as for the forward pass.  dA is summed in a fixed order.  Accuracy
+ * Scratch as for the forward pass, and 4 channels bytes for every chunk.  dA is
+ * summed in a fixed order.  Accuracy
  * against the fp64 gradients (from checkpoints: of the values that they stand for):
  * max abs error over max |value| <= 1e-5, plus half a step where bf16 is stored; for
  * dA, whose terms may cancel, 1e-5 of the largest sum of its terms' magnitudes.
@@ -491,7 +498,8 @@ SSD_API ssd_status_t ssd_glr_backward(const ssd_glr_dims_t *dims, const int64_t 
 /*
  * ssd_glr_step -- one token of the recurrence for every row: the decode step
  * on a resident state.  dims->seqlen must be 1; x_t, r_t, i_t, y_t [B, C]
- * dtype; state [B, C] fp32, read and overwritten with the new state; y_t must
+ * dtype; state [B, C] fp32, read and overwritten with the new state, rounded to fp32
+ * at every step (a decay closer to one than 2^-25 does not move it); y_t must
  * not alias the inputs or the state.  One launch, no allocation.
  */
 SSD_API ssd_status_t ssd_glr_step(const ssd_glr_dims_t *dims, const void *x_t, const void *r_t, const void *i_t,

@@ -590,7 +590,8 @@ def _unpack8(st, packed, dtype, out):
 def backward_packed8(x, dt, A, B, C, dy, D=None, chunk_len=256, init_state=None, dfinal_state=None, stream=None):
     """``backward`` from 8-bit checkpoints (``pack8``) of x, B and C through
     ``ssd_backward_packed8``: the gradients at the values that they stand for,
-    in dy's dtype.  Returns the dict of ``backward``."""
+    in dy's dtype.  Reads them back into scratch first.  Returns the dict of
+    ``backward``."""
     code, index = _storage("dy", dy)
     if dy.dim() != 4:
         raise ValueError("dy must be [batch, seqlen, nheads, headdim]")
@@ -640,8 +641,8 @@ def glr_forward(x, r, i, A, init_state=None, cu_seqlens=None, return_final_state
     """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(i_t) x_t with
     a_t = exp(A s(r_t)), s the logistic function, through ``ssd_glr_forward``.
 
-    x, r, i [B, T, C] (float32 or bfloat16, one dtype); A [C] float32, at most 0;
-    ``cu_seqlens`` (host: a list, a numpy array or a CPU tensor; B must be 1)
+    x, r, i [B, T, C] (float32 or bfloat16, one dtype; contiguous, on 16 bytes);
+    A [C] float32, at most 0; ``cu_seqlens`` (host: a list, a numpy array or a CPU tensor; B must be 1)
     holds nseq + 1 offsets of sequences packed along T; init_state and the final
     state are [B or nseq, C] float32.  ``save`` keeps what ``glr_backward`` needs:
     "inputs" refers to x, r and i themselves, "packed8" writes 8-bit
@@ -735,7 +736,7 @@ def _glr_backward(st, dims, dy, saved, packed, dfinal_state, return_dinit_state,
 def glr_step(state, x, r, i, A, out=None, stream=None):
     """One token of the gated linear recurrence through ``ssd_glr_step``: ``state``
     [B, C] float32 is updated in place and the output is returned.  x, r, i
-    [B, C] (float32 or bfloat16, one dtype); A [C] float32."""
+    [B, C] (float32 or bfloat16, one dtype; contiguous, on 16 bytes); A [C] float32."""
     code, index = _storage("x", x)
     shape, dtype = x.shape, x.dtype
     if len(shape) != 2:

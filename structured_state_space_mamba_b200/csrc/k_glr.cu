@@ -14,26 +14,27 @@
 // soon as it has them; a later tile looks back over at most four predecessors
 // to the nearest one whose outgoing state is known and applies the sums in
 // between in their order, so the bits do not depend on how far it looked.
-// Tiles are taken by ticket, chunk by chunk over all chains: a tile only ever
-// waits for one that a running block holds.
+// Tiles are taken by ticket, a batch's chunk by chunk over all rows, packed sequences
+// one after another: a tile only ever waits for one that a running block holds.
 //
 // A decay next to one, taken thousands of times, must not be rounded to a
-// multiple of 2^-24: a token works with e^l - 1, which keeps its own relative
-// precision (the recurrence is h + (e^l - 1) h + u), and the decay of several
-// tokens is the sum of their l until it is applied.  (As a product, it was off by
-// 1e-3 after 65536 tokens of constant gates, whose roundings all go one way.)
+// multiple of 2^-24: the decay of several tokens is the sum of their l until it is
+// applied, and applied as e^l - 1.  (As a running product, it was off by 1e-3 after
+// 65536 tokens of constant gates, whose roundings all go one way.)  Inside a tile
+// a state passes few tokens, and the decay is a factor; 1 - a^2 comes from e^l - 1.
 //
 // What bounds it.  Compulsory traffic is 8 bytes a value forwards in bf16 and 14
 // backwards (11 from checkpoints).  On 4 x 4096 x 5120 the forward pass takes
-// 140 us on the device, 4.8 TB/s: a pair of channels costs 72 instructions, of
-// which the packed ones (two cycles each) and the scalar ones fill the fp32 pipe
-// for about 65 cycles and eight special functions theirs for as many, of the 115
-// cycles that pass.  More warps did not change that (four groups of 56 registers:
-// 144 us; 16 warps of four tokens: 162 us), nor an earlier hand-out of the states.
-// Backwards it is 150 instructions and 16 special functions a pair, about twice the
-// time.  With few chains (1 x 65536 x 2048: 32 of them for 444 groups) the tiles of
-// a chain wait for each other's sums through L2: 336 us, 268 us with the sums of a
-// tile formed ahead (hold_ahead).
+// 144 us on the device, 4.7 TB/s, the backward pass 309 us (from checkpoints 421 us).
+// A pair of channels costs 72 instructions and 8 special functions forwards, 155 and 18
+// backwards (212 from checkpoints).  No unit is full: instructions issue in 55 to 58 % of
+// the cycles, DRAM is busy for 42 and 36 %.  What passes is latency: most of all
+// the wait of a tile for the state before it and, in a block, for the scan warp
+// to hand it out.  More warps did not change that (when the forward pass took 140 us:
+// four groups of 56 registers 144 us, 16 warps of four tokens 162 us), nor an earlier
+// hand-out of the states.  With few chains (1 x 65536 x 2048: 32 of them for 444 groups)
+// the tiles of a chain wait for each other's sums through L2: 338 us, 289 us with
+// the sums of a tile formed ahead (hold_ahead).
 #include "common.cuh"
 #include "glr.h"
 #include "pack8.cuh"
@@ -598,8 +599,10 @@ struct Tickets {
 //
 // Registers decide the shape: 27 warps leave 72 a thread, enough for a tile's
 // gates and no more.  Two groups that held two tiles each, to bridge the wait
-// themselves, spilled; next to this much shared memory L1 holds no spilled
-// words, and the backward pass took half as long again.
+// themselves, spilled all over their loops; next to this much shared memory L1
+// holds few spilled words, and the backward pass took half as long again.  Of the
+// kernels as they are, the backward ones from checkpoints and of odd rows in bf16
+// spill 28 to 124 bytes, the forward ones of odd rows in bf16 24 to 44.
 constexpr int kGroups = 3;
 constexpr int kBlock = kGroups * kGroupThreads;
 

@@ -15,9 +15,10 @@
 // cosines cost 1 / (2 G) of what they would a row.  Positions may be far: the
 // turns are two 64-bit numbers, and only their fraction becomes fp32.
 //
-// 65536 tokens x 8 groups x 128, bf16, slices of a projection: 93 us on the device,
-// 5.8 TB/s (125 us with scalar arithmetic and a load at a time; 101 us with six blocks
-// an SM, 96 us with eight, whose 64 registers spill).
+// 65536 tokens x 8 groups x 128, bf16, slices of a projection: 96 us on the device,
+// 5.6 TB/s.  (With one double an angle it was 93 us, against 125 us with scalar
+// arithmetic and a load at a time, 101 us with six blocks an SM, 96 us with eight, whose
+// 64 registers spill.)
 #include <math.h>
 
 #include "common.cuh"

@@ -23,7 +23,7 @@ def host(t):
 
 
 def on(a, dtype=torch.float32):
-    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(DEV).to(dtype)
+    return torch.from_numpy(np.array(a, dtype=np.float32, order="C")).to(DEV).to(dtype)
 
 
 def close(got, want, what, rel=1e-5):
