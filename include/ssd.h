@@ -554,8 +554,8 @@ SSD_API ssd_status_t ssd_norm_rotate(const ssd_rotate_dims_t *dims, const void *
  *   dw = sum over tokens and groups of dz xh,   d = dz w,
  *   dv = (d - xh mean(d xh)) / sqrt(mean v^2 + eps).
  * dB, dC [B, T, G, N] dtype, contiguous (must not alias the inputs);
- * dweight_B, dweight_C [N] fp32 or NULL (not computed), summed in a fixed
- * order through stream-ordered scratch of the library's pool.
+ * dweight_B, dweight_C [N] fp32 or NULL (not computed), summed in fp32 in a
+ * fixed order through stream-ordered scratch of the library's pool.
  */
 SSD_API ssd_status_t ssd_norm_rotate_backward(const ssd_rotate_dims_t *dims, const void *dB_out,
                                               const void *dC_out, const void *Bm, const void *Cm,
